@@ -456,6 +456,43 @@ def gdn_inputs(rng, b: int, t: int, h: int, dk: int = GDN_DK, dv: int = GDN_DV):
     return state, k, v, alpha, beta
 
 
+# ---------------------------------------------------------------- paged attention inputs
+@dataclass
+class PagedBatch:
+    """A ragged batch over a paged cache (fp16; pages in shuffled order)."""
+    q: np.ndarray           # fp16 [n, hq, d]
+    qkv: np.ndarray         # fp16 [n, (hq + 2 hkv) d]
+    k_cache: np.ndarray     # fp16 [pages, hkv, page, d]
+    v_cache: np.ndarray
+    table: np.ndarray       # int32 [b, max_pages], -1 behind a sequence's last page
+    cu: np.ndarray          # int32 [b + 1]
+    ctx: np.ndarray         # int32 [b]
+
+    @property
+    def max_q(self) -> int:
+        return int(np.max(np.diff(self.cu))) if len(self.ctx) else 0
+
+
+def paged_batch(rng, new, ctx, hq: int, hkv: int, d: int, page: int, spare: int = 2,
+                pad_rows: int = 0) -> PagedBatch:
+    """Sequences with ``new[b]`` rows and ``ctx[b]`` tokens; ``spare`` pages belong to none, and
+    ``pad_rows`` rows follow the last sequence."""
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    n = int(cu[-1]) + pad_rows
+    pages = [-(-int(c) // page) for c in ctx]
+    total = sum(pages) + spare
+    order = rng.permutation(total).astype(np.int32)
+    table = np.full((len(new), max([1] + pages)), -1, np.int32)
+    at = 0
+    for b, k in enumerate(pages):
+        table[b, :k] = order[at:at + k]
+        at += k
+    def f16(*shape):
+        return rng.standard_normal(shape, dtype=np.float32).astype(np.float16)
+    return PagedBatch(f16(n, hq, d), f16(n, (hq + 2 * hkv) * d), f16(total, hkv, page, d),
+                      f16(total, hkv, page, d), table, cu, np.asarray(ctx, np.int32))
+
+
 # ---------------------------------------------------------------- drafting inputs
 # Token histories for the prompt-lookup drafter ("Efficient LLM Challenge
 # Results", section 3: the n-gram drafter copies spans from the prompt; the

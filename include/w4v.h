@@ -292,6 +292,77 @@ int gdn_state_commit(float* state, const float* k, const float* v, const float* 
                      void* stream);
 
 /* ------------------------------------------------------------------------
+ * Attention of the target's layers over the verify block (section 3: the
+ * target's forward pass over the K + 1 positions) or a chunk of a prompt, on a
+ * paged key/value cache: rope_kv_append rotates the new queries and keys and
+ * writes the keys and values, paged_attention attends.
+ *
+ * Batch      ragged: rows cu[b] .. cu[b+1]-1 (int32 [B+1], ascending) are the
+ *            newest tokens of sequence b, whose ctx_lens[b] tokens (int32 [B])
+ *            include them, so row r sits at position ctx_lens[b] - cu[b+1] + r.
+ *            A row whose position is negative (more rows than tokens) has no
+ *            place: nothing of it is written by rope_kv_append, and
+ *            paged_attention gives zeros.  Rows at or behind cu[B] (a padded
+ *            batch) are left as they were.  cu and ctx_lens are read on the
+ *            device: a captured call follows their values at each replay.
+ * Cache      k_cache, v_cache fp16 [num_pages x Hkv x page_size x D], 16-byte
+ *            aligned, any size; block_table int32 [B x max_pages]: position p of
+ *            sequence b is slot p % page_size of page
+ *            block_table[b][p / page_size].  Entries that no position below
+ *            ctx_lens[b] needs are never read.  An entry outside [0, num_pages),
+ *            or a position past max_pages * page_size, never faults: such a key is
+ *            not stored, and no row sees it.  Pages may be shared by sequences for
+ *            reading; two rows written to one slot race.
+ * Sizes      D 64, 128 or 256; page_size a power of two, 16 .. 1024
+ *            (W4V_ERR_UNSUPPORTED otherwise); Hq a multiple of Hkv (query head j
+ *            reads key/value head j / (Hq / Hkv)); B <= 65535.  B == 0 or N == 0:
+ *            nothing to do.
+ * All pointers are device pointers; int32 and fp32 ones are 4-byte aligned.
+ * ---------------------------------------------------------------------- */
+
+/* Rotary positions and the append.
+ *   (x0, x1) -> (fp16_rne(m (x0 cos t - x1 sin t)), fp16_rne(m (x1 cos t + x0 sin t)))
+ *   with t = position * inv_freq[j] and m = mscale,
+ * for every pair j < rot/2 of every query and key head, the pair being elements
+ * (j, j + rot/2), or (2j, 2j+1) when interleaved != 0; elements rot .. D-1 are
+ * copied.  The product is formed and reduced in 64 bits.  A scaling for long
+ * contexts is a table inv_freq and its mscale.
+ * qkv        fp16 [N x (Hq + 2 Hkv) D] (the fused QKV linear's output: query, key,
+ *            value heads), row stride ldqkv; 16-byte aligned, ldqkv % 8 == 0.
+ * q_out      fp16 [N x Hq D] out, row stride ldq, the same alignment; either
+ *            qkv itself with ldq == ldqkv (in place) or not overlapping it.
+ * inv_freq   fp32 [rot/2] (may be NULL when rot == 0).
+ * rot        0 .. D, a multiple of 16 (W4V_ERR_UNSUPPORTED otherwise).
+ * The caches overlap neither each other nor qkv, q_out. */
+int rope_kv_append(const void* qkv, int64_t ldqkv, void* q_out, int64_t ldq,
+                   void* k_cache, void* v_cache, int num_pages, int page_size,
+                   const int32_t* block_table, int64_t max_pages, const int32_t* cu,
+                   const int32_t* ctx_lens, const float* inv_freq, float mscale,
+                   int N, int B, int Hq, int Hkv, int D, int rot, int interleaved, void* stream);
+
+/* Attention:  out[r, j] = sum_p w_p v_p,  w = softmax_p(scale * q[r, j] . k_p) over
+ * the positions p <= the row's own, fp32 scores, sums and running maxima, weights
+ * rounded to fp16 for the product with v, one fp16_rne of the result.  A row that
+ * sees no key gives zeros.
+ * q, out     fp16 [N x Hq D], row strides ldq, ldo; 16-byte aligned, strides
+ *            multiples of 8; out overlaps neither q nor the caches.
+ * scale      finite, > 0.
+ * max_q      the most rows a sequence has (rows of a sequence past max_q are left
+ *            as they were); max_ctx: the most tokens a sequence has, used for the
+ *            launch plan alone.  The plan, and so the order of sums, depends on
+ *            B, max_q, max_ctx, Hq, Hkv and D.
+ * workspace  paged_attention_workspace_size(...) bytes of scratch (0 for plans
+ *            that do not split the context; NULL then), 256-byte aligned, no
+ *            contents expected or kept. */
+size_t paged_attention_workspace_size(int B, int max_q, int max_ctx, int Hq, int Hkv, int D);
+
+int paged_attention(const void* q, int64_t ldq, const void* k_cache, const void* v_cache,
+                    int num_pages, int page_size, const int32_t* block_table, int64_t max_pages,
+                    const int32_t* cu, const int32_t* ctx_lens, void* out, int64_t ldo,
+                    int N, int B, int max_q, int max_ctx, int Hq, int Hkv, int D, float scale,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * A chain of W4A16 linears in one launch (section 3: the target's forward
  * pass over the verify block -- every linear of every layer -- at M <= 16
  * rows).  Linear l reads the leading K_l columns of linear l-1's output

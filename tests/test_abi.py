@@ -348,3 +348,103 @@ def gdnc(lib, s=A * 256, k=A, v=A * 2, al=A * 3, be=A * 4, acc=A * 5, B=2, T=16,
 ])
 def test_gdn_commit_validation(lib, kw, status):
     assert gdnc(lib, **kw) == status
+
+
+# ------------------------------------------------------------------ rotary positions, paged attention
+G = 1 << 32          # fake device ranges far from each other
+
+
+def rope(lib, qkv=G, ldqkv=6144, q=2 * G, ldq=4096, kc=3 * G, vc=5 * G, pages=100, page=64, table=A,
+         max_pages=32, cu=A, ctx=A, inv=A, N=16, B=1, Hq=32, Hkv=8, D=128, rot=128, inter=0):
+    return lib.rope_kv_append(qkv, ldqkv, q, ldq, kc, vc, pages, page, table, max_pages, cu, ctx, inv,
+                              ctypes.c_float(1.0), N, B, Hq, Hkv, D, rot, inter, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(N=0), OK), (dict(B=0), OK),
+    (dict(N=-1), INVALID), (dict(B=-1), INVALID), (dict(Hq=30), INVALID), (dict(Hkv=0), INVALID),
+    (dict(pages=0), INVALID), (dict(max_pages=0), INVALID), (dict(page=0), INVALID),
+    (dict(D=96), UNSUPPORTED), (dict(page=48), UNSUPPORTED), (dict(page=8), UNSUPPORTED),
+    (dict(page=2048), UNSUPPORTED), (dict(B=65536), UNSUPPORTED), (dict(rot=24), UNSUPPORTED),
+    (dict(rot=144), INVALID), (dict(rot=-16), INVALID), (dict(inv=None), INVALID),
+    (dict(qkv=None), INVALID), (dict(q=None), INVALID), (dict(kc=None), INVALID),
+    (dict(table=None), INVALID), (dict(cu=None), INVALID), (dict(ctx=None), INVALID),
+    (dict(ldqkv=6136), INVALID), (dict(ldq=4088), INVALID),
+    (dict(qkv=G + 8), ALIGN), (dict(q=2 * G + 8), ALIGN), (dict(ldqkv=6148), ALIGN),
+    (dict(ldq=4100), ALIGN), (dict(kc=3 * G + 8), ALIGN), (dict(vc=5 * G + 2), ALIGN),
+    (dict(table=A + 2), ALIGN), (dict(cu=A + 1), ALIGN), (dict(ctx=A + 2), ALIGN),
+    (dict(inv=A + 2), ALIGN),
+    (dict(q=G + 16, ldq=6144), INVALID),             # q_out overlaps qkv without being it
+    (dict(q=G, ldq=4096), INVALID),                  # the same start, another stride
+    (dict(vc=3 * G + 4096), INVALID),                # the caches overlap
+    (dict(kc=G + 256), INVALID), (dict(vc=2 * G), INVALID),
+])
+def test_rope_kv_append_validation(lib, kw, status):
+    assert rope(lib, **kw) == status
+
+
+def attn(lib, q=G, ldq=4096, kc=3 * G, vc=5 * G, pages=100, page=64, table=A, max_pages=32, cu=A,
+         ctx=A, out=2 * G, ldo=4096, N=16, B=1, max_q=16, max_ctx=100, Hq=32, Hkv=8, D=128, scale=0.1,
+         ws=A, wsb=1 << 30):
+    return lib.paged_attention(q, ldq, kc, vc, pages, page, table, max_pages, cu, ctx, out, ldo, N, B,
+                               max_q, max_ctx, Hq, Hkv, D, ctypes.c_float(scale), ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(N=0), OK), (dict(B=0), OK), (dict(max_q=0), OK),
+    (dict(N=-1), INVALID), (dict(max_q=-1), INVALID), (dict(max_ctx=-1), INVALID),
+    (dict(Hq=33), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
+    (dict(D=80), UNSUPPORTED), (dict(page=24), UNSUPPORTED), (dict(B=1 << 20), UNSUPPORTED),
+    (dict(max_q=1 << 30, N=1 << 30), UNSUPPORTED),
+    (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(kc=None), INVALID),
+    (dict(vc=None), INVALID), (dict(cu=None), INVALID), (dict(table=None), INVALID),
+    (dict(ldq=4000), INVALID), (dict(ldo=4000), INVALID),
+    (dict(q=G + 8), ALIGN), (dict(out=2 * G + 4), ALIGN), (dict(ldo=4100), ALIGN),
+    (dict(kc=3 * G + 4), ALIGN), (dict(ctx=A + 1), ALIGN),
+    (dict(out=G), INVALID), (dict(out=G + 4096), INVALID), (dict(out=3 * G), INVALID),
+    (dict(out=5 * G + 64), INVALID),
+])
+def test_paged_attention_validation(lib, kw, status):
+    assert attn(lib, **kw) == status
+
+
+def test_paged_attention_workspace(lib):
+    need = w4v.paged_attention_workspace_size(1, 16, 8208, 32, 8, 128)
+    assert need > 0                                  # few blocks: the context is split
+    long = dict(max_ctx=8208, max_pages=200)
+    assert attn(lib, **long, ws=None, wsb=0) == WORKSPACE
+    assert attn(lib, **long, wsb=need - 1) == WORKSPACE
+    assert attn(lib, **long, ws=A + 16, wsb=need) == ALIGN
+    # enough blocks without a split: no workspace; nonsense: none either
+    assert w4v.paged_attention_workspace_size(1, 8192, 8192, 32, 8, 128) == 0
+    assert w4v.paged_attention_workspace_size(64, 1, 100, 32, 8, 128) == 0
+    assert w4v.paged_attention_workspace_size(0, 16, 8208, 32, 8, 128) == 0
+    assert w4v.paged_attention_workspace_size(1, 16, 8208, 32, 8, 96) == 0
+
+
+def test_rope_frequency_tables():
+    """The scaled tables against their formulas, pair by pair."""
+    import math
+
+    import torch
+    f, m = w4v.rope_inv_freq(64, base=1e4, device="cpu")
+    assert m == 1.0 and f.dtype == torch.float32
+    for j in range(32):
+        assert math.isclose(float(f[j]), 1e4 ** (-2 * j / 64), rel_tol=2**-24)
+    g, _ = w4v.rope_inv_freq(64, scaling="linear", factor=4.0, device="cpu")
+    assert torch.equal(g * 4, f)
+    n, _ = w4v.rope_inv_freq(64, scaling="ntk", factor=4.0, device="cpu")
+    assert n[0] == f[0] and math.isclose(float(n[-1]), float(f[-1]) / 4, rel_tol=1e-6)
+    y, my = w4v.rope_inv_freq(64, scaling="yarn", factor=4.0, original_context=4096, device="cpu")
+    assert math.isclose(my, 1 + 0.1 * math.log(4))
+    turns = f.double() * 4096 / (2 * math.pi)
+    assert torch.equal(y[turns > 33], f[turns > 33])          # fast pairs are kept
+    slow = turns < 0.9
+    assert slow.any() and torch.allclose(y[slow] * 4, f[slow], rtol=1e-6)
+    r = y / f
+    assert torch.all(r[1:] <= r[:-1] + 1e-6)
+    assert w4v.rope_inv_freq(0, device="cpu")[0].numel() == 0
+    for bad in (dict(rot=3), dict(rot=-2), dict(rot=8, factor=0.0), dict(rot=8, scaling="cubic")):
+        with pytest.raises(ValueError):
+            w4v.rope_inv_freq(device="cpu", **bad)

@@ -1,0 +1,345 @@
+"""GPU parity of rotary positions with the cache append, and of attention over
+the paged cache, against the fp64 oracle.
+
+Tolerances, element by element, from the roundings that the operators make:
+  rotation   one fp16 rounding of the result (2^-11 of it, 2^-25 where it is
+             subnormal) and fp32 arithmetic on cos and sin, whose angle is
+             reduced in 64 bits: 2^-20 (|x0| + |x1|) m covers the reduction's
+             fp32 remainder (2^-23 turns, 2.6 ulp), sincospif, the scaling by m
+             and three roundings of the products and the sum.
+  attention  with w the exact weights: every weight is off by at most
+             e = 2 d + 2^-11 relative, d the error of its exponent -- a dot
+             product of D terms, D 2^-24 scale sum |q||k|, its scaling and
+             subtraction 2^-22 of the largest |score|, exp2 2^-22 -- entering
+             the numerator and the sum, and 2^-11 its rounding to fp16; both sums
+             run over n keys in fp32, n 2^-23.  The result is rounded to fp16 once.
+             |error| <= (e + n 2^-23) sum w|v| + 2^-11 |o| + 2^-25.
+"""
+import numpy as np
+import pytest
+
+import gen
+from oracle import attention as oa
+from tests.gpu_util import dev, host, log
+
+pytestmark = pytest.mark.gpu
+
+
+def check_attention(got, q, ref, d, scale, what):
+    out, spread, reach, seen = ref
+    got = np.asarray(got, np.float64)
+    live = ~np.isnan(out[:, 0, 0])
+    dd = d * 2.0**-24 * scale * reach + 2.0**-22 * (1 + scale * reach)
+    e = 2 * dd + 2.0**-11 + seen[:, None] * 2.0**-23
+    tol = e[:, :, None] * spread + 2.0**-11 * np.abs(out) + 2.0**-25
+    err = np.abs(got - out)[live]
+    assert np.all(np.isfinite(got[live])), what
+    worst = np.max(err / tol[live]) if err.size else 0.0
+    assert worst <= 1.0, f"{what}: {worst:.2f} of the tolerance"
+    return worst
+
+
+def run_attention(lib, x, scale=None, **kw):
+    import torch
+    d = x.q.shape[-1]
+    out = torch.full(x.q.shape, 7.0, dtype=torch.float16, device="cuda")
+    got = lib.paged_attention(dev(x.q), dev(x.k_cache), dev(x.v_cache), dev(x.table), dev(x.cu),
+                              dev(x.ctx), x.max_q, scale=scale, out=out, **kw)
+    torch.cuda.synchronize()
+    scale = d ** -0.5 if scale is None else scale
+    ref = oa.attention(x.q, x.k_cache, x.v_cache, x.table, x.cu, x.ctx, scale)
+    got = host(got)
+    w = check_attention(got, x.q, ref, d, scale, "attention")
+    n = int(x.cu[-1])
+    assert np.all(got[n:] == 7.0), "rows behind the last sequence were written"
+    return got, w
+
+
+@pytest.mark.parametrize("new,ctx,hq,hkv,d,page", [
+    ([1], [1], 4, 1, 128, 16),                                # one token that sees itself
+    ([1], [1001], 8, 2, 128, 16),
+    ([1, 1, 1], [15, 16, 17], 4, 4, 64, 16),                  # page and group borders
+    ([1, 1, 1, 1], [31, 32, 33, 65], 16, 1, 128, 32),         # 16 heads on one key head
+    ([2, 5, 3], [40, 5, 129], 5, 1, 64, 64),                  # an odd group; a prompt of its own
+    ([16], [300], 8, 2, 128, 64),                             # 64 packed rows
+    ([16, 16], [500, 16], 4, 1, 256, 16),
+    ([21, 21, 21], [130, 64, 700], 8, 2, 128, 16),            # 84 packed rows
+    ([21, 7], [90, 333], 6, 2, 64, 128),
+    ([70, 130], [200, 130], 4, 2, 128, 32),                   # prompt chunks
+    ([190], [1000], 4, 2, 64, 256),
+    ([100], [161], 3, 1, 256, 1024),
+    ([300, 1, 33], [300, 700, 40], 4, 1, 128, 16),            # mixed prompt and decode
+])
+def test_attention_matches_oracle(lib, new, ctx, hq, hkv, d, page):
+    rng = np.random.default_rng(sum(new) * 7 + sum(ctx) + d)
+    x = gen.paged_batch(rng, new, ctx, hq, hkv, d, page)
+    _, w = run_attention(lib, x)
+    log(f"  {new} {ctx} {hq}/{hkv} d={d} page={page}: {w:.2f} of the tolerance")
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 4, 16, 40])
+def test_context_split_over_blocks(lib, d, new):
+    """Few sequences and a long context: blocks share a context and are joined."""
+    rng = np.random.default_rng(d + new)
+    x = gen.paged_batch(rng, [new, new], [5003, 2100], 4, 1, d, 32)
+    assert lib.paged_attention_workspace_size(2, new, 5003, 4, 1, d) > 0
+    run_attention(lib, x, max_ctx=5003)
+
+
+def test_empty_rows_sequences_and_padding(lib):
+    """No tokens, no rows, more rows than tokens (rows before position 0 give zeros), rows behind
+    the last sequence (left alone), and a first sequence that does not start at row 0."""
+    rng = np.random.default_rng(3)
+    x = gen.paged_batch(rng, [3, 0, 5, 1, 4], [3, 40, 2, 0, 200], 4, 2, 64, 16, pad_rows=6)
+    got, _ = run_attention(lib, x)
+    assert np.all(got[3:6] == 0) and np.all(got[8] == 0)      # 5 rows on 2 tokens; no token at all
+    assert np.any(got[6:8] != 0)
+
+
+def test_unused_places_may_hold_anything(lib):
+    """NaN and infinities in free pages, behind a sequence's last token and in table entries that
+    nothing needs."""
+    rng = np.random.default_rng(4)
+    for page, d in ((16, 128), (64, 64), (128, 256)):
+        x = gen.paged_batch(rng, [1, 5, 20], [37, 65, 130], 4, 2, d, page, spare=3)
+        clean, _ = run_attention(lib, x)
+        used = np.zeros(x.k_cache.shape[0::2], bool)          # [pages, page]
+        for b, c in enumerate(x.ctx):
+            for p in range(c):
+                used[x.table[b, p // page], p % page] = True
+        free = int((~used).sum())
+        for cache in (x.k_cache, x.v_cache):
+            bad = np.resize(np.array([np.nan, np.inf, -np.inf, 65504], np.float16), free)
+            cache.transpose(0, 2, 1, 3)[~used] = bad[:, None, None]
+        x.table[x.table < 0] = 2**31 - 1
+        got, _ = run_attention(lib, x)
+        assert np.array_equal(got, clean)
+
+
+def test_pages_outside_the_cache_are_not_seen(lib):
+    """Entries inside the context that point nowhere, and a context longer than its table."""
+    rng = np.random.default_rng(5)
+    x = gen.paged_batch(rng, [2, 17, 1], [100, 150, 90], 4, 2, 128, 16)
+    x.table[0, 2] = -1
+    x.table[1, 0] = x.k_cache.shape[0]
+    x.table[1, 5] = -2**31
+    x.table[2, :] = 1 << 30                                   # nothing left: zeros
+    x.ctx[1] = 150
+    got, _ = run_attention(lib, x)
+    assert np.all(got[19] == 0)
+    x.ctx[0] = x.table.shape[1] * 16 + 40                     # positions past the table
+    run_attention(lib, x)
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "wide"])
+def test_moving_maxima(lib, order):
+    """Scores that rise by hundreds along the context (the running maximum moves at nearly every
+    tile), fall, or jump: no overflow, no lost weight."""
+    rng = np.random.default_rng(6)
+    x = gen.paged_batch(rng, [1, 18], [900, 700], 2, 1, 64, 16)
+    x.q[:] = np.float16(1.0)
+    for b, c in enumerate(x.ctx):
+        for p in range(c):
+            s = {"rising": p / 60.0, "falling": -p / 60.0, "wide": rng.choice([-6.0, 0.0, 6.0])}[order]
+            x.k_cache[x.table[b, p // 16], :, p % 16] = np.float16(s)
+    run_attention(lib, x, scale=0.5)
+
+
+def test_strided_rows(lib):
+    """q as the query columns of fused rows, out as columns of a wider buffer."""
+    import torch
+    rng = np.random.default_rng(7)
+    x = gen.paged_batch(rng, [9, 30], [60, 400], 4, 2, 128, 32)
+    want, _ = run_attention(lib, x)
+    n, hq, d = x.q.shape
+    wide = torch.full((n, hq * d + 264), float("nan"), dtype=torch.float16, device="cuda")
+    wide[:, 8:8 + hq * d] = dev(x.q).view(n, -1)
+    outw = torch.full((n, hq * d + 72), 5.0, dtype=torch.float16, device="cuda")
+    lib.paged_attention(wide[:, 8:8 + hq * d].view(n, hq, d), dev(x.k_cache), dev(x.v_cache),
+                        dev(x.table), dev(x.cu), dev(x.ctx), x.max_q,
+                        out=outw[:, 64:64 + hq * d].view(n, hq, d))
+    torch.cuda.synchronize()
+    assert np.array_equal(host(outw)[:, 64:64 + hq * d].reshape(n, hq, d), want)
+    assert np.all(host(outw)[:, :64] == 5) and np.all(host(outw)[:, 64 + hq * d:] == 5)
+
+
+def test_cache_longer_than_32_bit_offsets(lib):
+    """Pages past 4 GiB of a cache."""
+    import torch
+    rng = np.random.default_rng(8)
+    x = gen.paged_batch(rng, [1, 3], [50, 70], 4, 4, 128, 64, spare=0)
+    pages = (5 << 30) // (4 * 64 * 128 * 2)
+    big = [torch.empty((pages, 4, 64, 128), dtype=torch.float16, device="cuda") for _ in range(2)]
+    at = pages - x.k_cache.shape[0]
+    for t, c in zip(big, (x.k_cache, x.v_cache)):
+        t[at:] = dev(c)
+    table = np.where(x.table >= 0, x.table + at, -1).astype(np.int32)
+    got = lib.paged_attention(dev(x.q), *big, dev(table), dev(x.cu), dev(x.ctx), x.max_q)
+    want, _ = run_attention(lib, x)
+    assert np.array_equal(host(got), want)
+    # and the append there
+    inv, m = lib.rope_inv_freq(128)
+    lib.rope_kv_append(dev(x.qkv), *big, dev(table), dev(x.cu), dev(x.ctx), inv, 4, mscale=m)
+    ks, vs = dev(x.k_cache), dev(x.v_cache)
+    lib.rope_kv_append(dev(x.qkv), ks, vs, dev(x.table), dev(x.cu), dev(x.ctx), inv, 4, mscale=m)
+    torch.cuda.synchronize()
+    assert torch.equal(big[0][at:], ks) and torch.equal(big[1][at:], vs)
+
+
+# ------------------------------------------------------------------ rotation and append
+def check_rope(lib, x, inv, hq, mscale, interleaved, q_out=None, qkv=None):
+    import torch
+    k, v = dev(x.k_cache), dev(x.v_cache)
+    hkv, d = x.k_cache.shape[1], x.k_cache.shape[3]
+    n = x.qkv.shape[0]
+    if q_out is None:
+        q_out = torch.full((n, hq, d), 9.0, dtype=torch.float16, device="cuda")
+    before = host(q_out).copy()
+    got = lib.rope_kv_append(dev(x.qkv) if qkv is None else qkv, k, v, dev(x.table), dev(x.cu),
+                             dev(x.ctx), inv, hq, interleaved=interleaved, mscale=mscale, q_out=q_out)
+    torch.cuda.synchronize()
+    f = host(inv)
+    qr, kr, vr = oa.rope_append(x.qkv, x.k_cache, x.v_cache, x.table, x.cu, x.ctx, f, hq, mscale,
+                                interleaved)
+    rot = 2 * len(f)
+    size = np.abs(x.qkv.astype(np.float64)).max()
+    got = host(got).reshape(n, hq, d)
+    live = ~np.isnan(qr[:, 0, 0])
+    assert np.array_equal(got[~live].ravel(), before.reshape(n, hq, d)[~live].ravel())
+    for g, r in ((got[live], qr[live]), (host(k), kr)):
+        tol = 2.0**-11 * np.abs(r) + 2.0**-25 + 2.0**-20 * 2 * size * mscale
+        assert np.all(np.abs(g.astype(np.float64) - r) <= tol), np.max(np.abs(g - r) / tol)
+        assert np.array_equal(g[..., rot:], r[..., rot:].astype(np.float16))
+    assert np.array_equal(host(v), vr.astype(np.float16))
+    return got
+
+
+@pytest.mark.parametrize("new,ctx,hq,hkv,d,rot,inter,page", [
+    ([1], [1], 4, 1, 128, 128, False, 16),
+    ([16, 16], [2048, 16], 32, 8, 128, 128, False, 64),
+    ([3, 0, 9], [17, 5, 33], 5, 1, 64, 32, True, 16),
+    ([21, 2], [60, 700], 6, 2, 256, 64, False, 32),
+    ([40], [1000], 2, 2, 256, 256, True, 128),
+    ([7, 1], [7, 1], 8, 8, 64, 16, True, 16),
+    ([5], [20], 3, 1, 128, 0, False, 16),                     # no rotation: the append alone
+])
+def test_rope_append_matches_oracle(lib, new, ctx, hq, hkv, d, rot, inter, page):
+    rng = np.random.default_rng(sum(new) + d + rot)
+    x = gen.paged_batch(rng, new, ctx, hq, hkv, d, page, pad_rows=2)
+    inv, m = lib.rope_inv_freq(rot, scaling="yarn" if rot else "none", factor=4.0)
+    check_rope(lib, x, inv, hq, m, inter)
+
+
+def test_rope_far_positions(lib):
+    """Positions of a million tokens: the angle keeps its fraction of a turn."""
+    rng = np.random.default_rng(11)
+    x = gen.paged_batch(rng, [4], [64], 2, 1, 64, 16)
+    far = 1_048_576 + 37
+    pages = -(-far // 16)
+    table = np.full((1, pages), -1, np.int32)
+    table[0, -4:] = [0, 1, 2, 3]
+    x.table, x.ctx = table, np.array([far], np.int32)
+    inv, m = lib.rope_inv_freq(64, base=1e6)
+    check_rope(lib, x, inv, 2, m, False)
+
+
+def test_rope_in_place_strided_and_unplaced(lib):
+    """q_out = the query columns of the fused rows; rows before position 0; pages outside the cache
+    and positions past the table are rotated but not stored."""
+    import torch
+    rng = np.random.default_rng(12)
+    x = gen.paged_batch(rng, [5, 8, 3], [2, 40, 30], 4, 2, 64, 16)
+    x.table[1, 2] = 999
+    x.ctx[2] = x.table.shape[1] * 16 + 1
+    inv, m = lib.rope_inv_freq(64)
+    want = check_rope(lib, x, inv, 4, m, False)
+    wide = torch.zeros((16, 8 * 64 + 40), dtype=torch.float16, device="cuda")
+    wide[:, :512] = dev(x.qkv)
+    got = check_rope(lib, x, inv, 4, m, False, q_out=wide[:, :256], qkv=wide)
+    live = [r for r in range(16) if r >= 3]                    # rows 0..2 lie before position 0
+    assert np.array_equal(got[live], want[live])
+    assert torch.equal(wide[:, 256:512], dev(x.qkv)[:, 256:])
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("use_stream", [False, True])
+def test_append_then_attend_over_blocks(lib, use_stream):
+    """Prompt, then verify blocks in turn, as they are used: each block's keys go to the cache, the
+    block attends, some drafts are rejected and the next block overwrites their places."""
+    import torch
+    rng = np.random.default_rng(13)
+    hq, hkv, d, page, B, K = 8, 2, 128, 16, 3, 7
+    pages = 12
+    kc = rng.standard_normal((B * pages, hkv, page, d)).astype(np.float16)
+    vc = rng.standard_normal((B * pages, hkv, page, d)).astype(np.float16)
+    table = rng.permutation(B * pages).astype(np.int32).reshape(B, pages)
+    kd, vd, td = dev(kc), dev(vc), dev(table)
+    inv, m = lib.rope_inv_freq(d, scaling="linear", factor=2.0)
+    stream = torch.cuda.Stream() if use_stream else None
+    lens = np.zeros(B, np.int64)
+    for step in range(4):
+        new = np.array([20, 33, 5]) if step == 0 else np.full(B, K + 1)
+        ctx = (lens + new).astype(np.int32)
+        cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        qkv = rng.standard_normal((int(cu[-1]), (hq + 2 * hkv) * d)).astype(np.float16)
+        args = dev(qkv), dev(cu), dev(ctx)
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        q = lib.rope_kv_append(args[0], kd, vd, td, args[1], args[2], inv, hq, mscale=m, stream=stream)
+        o = lib.paged_attention(q, kd, vd, td, args[1], args[2], int(new.max()), stream=stream)
+        torch.cuda.synchronize()
+        k_np, v_np, q_np = host(kd), host(vd), host(q)
+        qr, kr, vr = oa.rope_append(qkv, kc, vc, table, cu, ctx, host(inv), hq, m)
+        assert np.allclose(k_np, kr, rtol=2**-10, atol=2**-17) and np.array_equal(v_np, vr)
+        check_attention(host(o), q_np, oa.attention(q_np, k_np, v_np, table, cu, ctx, d ** -0.5), d,
+                        d ** -0.5, f"step {step}")
+        kc, vc = k_np, v_np
+        lens += new if step == 0 else rng.integers(1, K + 2, B)
+
+
+def test_captured_calls_follow_the_lengths(lib):
+    """A graph of append + attention, replayed with other lengths and inputs, with eager calls and
+    synchronizations between, equals the eager calls each time."""
+    import torch
+    rng = np.random.default_rng(14)
+    hq, hkv, d, page, B, T = 8, 2, 128, 32, 2, 4
+    x = gen.paged_batch(rng, [T, T], [3000, 2500], hq, hkv, d, page)
+    kd, vd, td, cu = dev(x.k_cache), dev(x.v_cache), dev(x.table), dev(x.cu)
+    ctx, qkv = dev(x.ctx), dev(x.qkv)
+    inv, m = lib.rope_inv_freq(d)
+    q = torch.empty((B * T, hq, d), dtype=torch.float16, device="cuda")
+    o = torch.empty_like(q)
+    ws = lib.new_workspace(lib.paged_attention_workspace_size(B, T, 3000, hq, hkv, d))
+
+    def step(q, o, ws):
+        lib.rope_kv_append(qkv, kd, vd, td, cu, ctx, inv, hq, mscale=m, q_out=q)
+        lib.paged_attention(q, kd, vd, td, cu, ctx, T, max_ctx=3000, out=o, workspace=ws)
+
+    step(q, o, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(q, o, ws)
+    q2, o2 = torch.empty_like(q), torch.empty_like(o)
+    for lens in ([3000, 2500], [2999, 7], [4, 4], [3000, 1]):
+        ctx.copy_(torch.tensor(lens, dtype=torch.int32))
+        qkv.copy_(dev(rng.standard_normal(x.qkv.shape).astype(np.float16)))
+        o.fill_(3.0)
+        g.replay()
+        torch.cuda.synchronize()
+        got = o.clone()
+        o2.fill_(3.0)
+        step(q2, o2, None)
+        torch.cuda.synchronize()
+        assert torch.equal(got, o2), lens
+
+
+def test_repeats_are_bit_identical(lib):
+    import torch
+    rng = np.random.default_rng(15)
+    x = gen.paged_batch(rng, [16], [2000], 8, 2, 128, 16)
+    args = [dev(a) for a in (x.q, x.k_cache, x.v_cache, x.table, x.cu, x.ctx)]
+    first = lib.paged_attention(*args, 16)
+    for _ in range(5):
+        assert torch.equal(lib.paged_attention(*args, 16), first)

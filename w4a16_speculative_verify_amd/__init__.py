@@ -56,6 +56,12 @@ SIGNATURES = {
     "f16_lmhead_argmax_verify": (_int, [_vp, _i64, _vp, _vp, _vp, _int, _int, _int, _vp, _int,
                                         _int, _vp, _vp, _vp, _sz, _vp]),
     "gdn_state_commit": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _int, _int, _int, _int, _vp]),
+    "rope_kv_append": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _int, _int, _vp, _i64, _vp, _vp, _vp,
+                              ctypes.c_float, _int, _int, _int, _int, _int, _int, _int, _vp]),
+    "paged_attention_workspace_size": (_sz, [_int] * 6),
+    "paged_attention": (_int, [_vp, _i64, _vp, _vp, _int, _int, _vp, _i64, _vp, _vp, _vp, _i64,
+                               _int, _int, _int, _int, _int, _int, _int, ctypes.c_float, _vp, _sz,
+                               _vp]),
     "f16_gemm_workspace_size": (_sz, [_int, _int, _int]),
     "f16_gemm": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _int, _int, _int, ctypes.c_float, _vp,
                         _sz, _vp]),
@@ -458,6 +464,171 @@ class Chain:
         """The kernel's error word (synchronises): 0 ok, 1 wait timed out, 2 not prepared."""
         w = self.workspace[CHAIN_ERROR_OFFSET:CHAIN_ERROR_OFFSET + 4]
         return int(w.cpu().view(__import__("torch").int32).item())
+
+
+# ------------------------------------------------------------------- attention
+def _elsewhere(t, stream):
+    """Whether a call has to enter another device or stream first (its own allocations then belong
+    to that stream)."""
+    import torch
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return stream is not None or t.device.index != torch.cuda.current_device()
+
+
+def _on_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _paged(k_cache, v_cache, block_table, cu, ctx_lens):
+    """(pages, kv heads, page size, head width, sequences) of a paged cache and its batch."""
+    torch = _require(k_cache, __import__("torch").float16, "k_cache")
+    _require(v_cache, torch.float16, "v_cache")
+    for t, name in ((block_table, "block_table"), (cu, "cu"), (ctx_lens, "ctx_lens")):
+        _require(t, torch.int32, name)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must both be [pages, kv heads, page size, D]")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be contiguous")
+    b = ctx_lens.shape[0]
+    if ctx_lens.dim() != 1 or tuple(cu.shape) != (b + 1,):
+        raise ValueError("cu must have one entry more than ctx_lens")
+    if block_table.dim() != 2 or block_table.shape[0] != b:
+        raise ValueError("block_table must be [B, max_pages]")
+    return (*k_cache.shape, b)
+
+
+def rope_inv_freq(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                  original_context: int = 8192, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                  device="cuda"):
+    """(inv_freq fp32 [rot/2], mscale) for rope_kv_append.
+
+    scaling "none": base^(-2j/rot); "linear": those divided by ``factor`` (positions
+    interpolated); "ntk": base * factor^(rot/(rot-2)), which keeps the fastest pair and divides
+    the slowest by ``factor``; "yarn": pairs that turn more than ``beta_fast`` times over
+    ``original_context`` are kept, those below ``beta_slow`` turns divided by ``factor``, a linear
+    ramp over the pair index between, and mscale 1 + 0.1 ln(factor).
+    """
+    import math
+
+    import torch
+    if rot < 0 or rot % 2 or factor <= 0:
+        raise ValueError("rot must be even and not negative, factor positive")
+    if scaling not in ("none", "linear", "ntk", "yarn"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    e = torch.arange(0, rot, 2, dtype=torch.float64)
+    mscale = 1.0
+    if scaling == "ntk" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-e / max(rot, 1))
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn" and rot > 0:
+        def pair_of(turns):                  # the pair that turns so often over the context
+            return rot * math.log(original_context / (turns * 2 * math.pi)) / (2 * math.log(base))
+        lo = max(math.floor(pair_of(beta_fast)), 0)
+        hi = min(math.ceil(pair_of(beta_slow)), rot - 1)
+        keep = 1 - ((e / 2 - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+        mscale = 1.0 + 0.1 * math.log(factor) if factor > 1 else 1.0
+    return f.to(torch.float32).to(device), mscale
+
+
+def rope_kv_append(qkv, k_cache, v_cache, block_table, cu, ctx_lens, inv_freq, hq: int,
+                   interleaved: bool = False, mscale: float = 1.0, q_out=None, stream=None):
+    """Rotate the queries and keys of fused QKV rows and append keys and values to a paged cache.
+
+    qkv fp16 [N, >= (hq + 2 hkv) * D] (rows may be strided); k_cache, v_cache fp16 [pages, hkv,
+    page_size, D], written in place; block_table int32 [B, max_pages]; cu int32 [B + 1]: sequence
+    b's new rows; ctx_lens int32 [B]: its tokens, the new ones included; inv_freq fp32 [rot/2]
+    (rope_inv_freq).  Returns q_out fp16 [N, hq, D] (``q_out`` may be qkv[:, :hq * D] itself);
+    rows that belong to no sequence or lie before position 0 are not written.
+    """
+    if _elsewhere(qkv, stream):
+        import torch
+        with torch.cuda.device(qkv.device), torch.cuda.stream(stream):
+            return rope_kv_append(qkv, k_cache, v_cache, block_table, cu, ctx_lens, inv_freq, hq,
+                                  interleaved, mscale, q_out)
+    torch = _require(qkv, __import__("torch").float16, "qkv")
+    pages, hkv, page, d, b = _paged(k_cache, v_cache, block_table, cu, ctx_lens)
+    _require(inv_freq, torch.float32, "inv_freq")
+    if qkv.dim() != 2 or qkv.shape[1] < (hq + 2 * hkv) * d:
+        raise ValueError(f"qkv must be [N, >= {(hq + 2 * hkv) * d}], got {tuple(qkv.shape)}")
+    n = qkv.shape[0]
+    if q_out is None:
+        q_out = torch.empty((n, hq, d), dtype=torch.float16, device=qkv.device)
+    _require(q_out, torch.float16, "q_out")
+    if q_out.shape[0] != n or q_out.numel() != n * hq * d or \
+            (q_out.dim() == 3 and q_out.stride(1) != d and q_out.shape[1] > 1):
+        raise ValueError(f"q_out must be [{n}, {hq}, {d}] or [{n}, {hq * d}], heads contiguous")
+    _on_device(qkv.device, k_cache=k_cache, v_cache=v_cache, block_table=block_table, cu=cu,
+               ctx_lens=ctx_lens, inv_freq=inv_freq, q_out=q_out)
+    if not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be contiguous")
+    st = load().rope_kv_append(
+        _ptr(qkv), _ld(qkv, (hq + 2 * hkv) * d), _ptr(q_out), _ld(q_out, hq * d), _ptr(k_cache),
+        _ptr(v_cache), pages, page, _ptr(block_table), block_table.shape[1], _ptr(cu), _ptr(ctx_lens), _ptr(inv_freq),
+        ctypes.c_float(mscale), n, b, hq, hkv, d, 2 * inv_freq.numel(), int(interleaved), _stream())
+    _check(st, "rope_kv_append")
+    return q_out
+
+
+def _ld(t, width):
+    """Row stride of a tensor whose rows are its first dimension (the width for a single row, whose
+    stride says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def paged_attention_workspace_size(b: int, max_q: int, max_ctx: int, hq: int, hkv: int,
+                                   d: int) -> int:
+    return int(load().paged_attention_workspace_size(b, max_q, max_ctx, hq, hkv, d))
+
+
+def paged_attention(q, k_cache, v_cache, block_table, cu, ctx_lens, max_q: int, max_ctx=None,
+                    scale=None, out=None, workspace=None, stream=None):
+    """Softmax attention of the new rows q fp16 [N, hq, D] over all tokens of their sequences at or
+    before them, read from the paged cache (the arguments of rope_kv_append).
+
+    ``max_q``: the most rows a sequence has; ``max_ctx``: the most tokens (the table's room by
+    default; it shapes the launch, not the result); ``scale`` D^-0.5 by default.  q's and out's
+    rows may be strided.  Returns out fp16 [N, hq, D]; rows that see no token are zeros, rows
+    behind the last sequence are not written.
+    """
+    if _elsewhere(q, stream):
+        import torch
+        with torch.cuda.device(q.device), torch.cuda.stream(stream):
+            return paged_attention(q, k_cache, v_cache, block_table, cu, ctx_lens, max_q, max_ctx,
+                                   scale, out, workspace)
+    torch = _require(q, __import__("torch").float16, "q")
+    pages, hkv, page, d, b = _paged(k_cache, v_cache, block_table, cu, ctx_lens)
+    if q.dim() != 3 or q.shape[2] != d or (q.shape[1] > 1 and q.stride(1) != d):
+        raise ValueError(f"q must be [N, heads, {d}], heads contiguous, got {tuple(q.shape)}")
+    n, hq = q.shape[0], q.shape[1]
+    if out is None:
+        out = torch.empty((n, hq, d), dtype=torch.float16, device=q.device)
+    _require(out, torch.float16, "out")
+    if out.shape[0] != n or out.numel() != n * hq * d or \
+            (out.dim() == 3 and out.stride(1) != d and hq > 1):
+        raise ValueError(f"out must be [{n}, {hq}, {d}] or [{n}, {hq * d}], heads contiguous")
+    if max_ctx is None:
+        max_ctx = min(block_table.shape[1] * page, 2**31 - 1)
+    need = paged_attention_workspace_size(b, max_q, max_ctx, hq, hkv, d)
+    if workspace is None and need > 0:
+        workspace = new_workspace(need, q.device)
+    _on_device(q.device, k_cache=k_cache, v_cache=v_cache, block_table=block_table, cu=cu,
+               ctx_lens=ctx_lens, out=out, workspace=workspace)
+    wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = load().paged_attention(
+        _ptr(q), _ld(q, hq * d), _ptr(k_cache), _ptr(v_cache), pages, page, _ptr(block_table),
+        block_table.shape[1], _ptr(cu), _ptr(ctx_lens), _ptr(out), _ld(out, hq * d), n, b, max_q, max_ctx,
+        hq, hkv, d, ctypes.c_float(d ** -0.5 if scale is None else scale), _ptr(workspace), wbytes,
+        _stream())
+    _check(st, "paged_attention")
+    return out
 
 
 # ------------------------------------------------------------------- drafting

@@ -574,6 +574,144 @@ int gdn_state_commit(float* state, const float* k, const float* v, const float* 
   return e == hipSuccess ? W4V_OK : W4V_ERR_HIP;
 }
 
+namespace {
+
+// the checks rope_kv_append and paged_attention share; *shift: log2 of the page size
+int paged_check(const void* k_cache, const void* v_cache, int num_pages, int page_size,
+                const int32_t* block_table, int64_t max_pages, const int32_t* cu,
+                const int32_t* ctx_lens, int Hq, int Hkv, int D, int* shift, size_t* cache_bytes) {
+  if (!k_cache || !v_cache || !block_table || !cu || !ctx_lens) return W4V_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_table, 4) ||
+      !aligned(cu, 4) || !aligned(ctx_lens, 4))
+    return W4V_ERR_ALIGNMENT;
+  *shift = 0;
+  while ((1 << *shift) < page_size) ++*shift;
+  *cache_bytes = (size_t)num_pages * Hkv * page_size * D * 2;
+  return W4V_OK;
+}
+
+int paged_sizes(int N, int B, int Hq, int Hkv, int D, int num_pages, int page_size,
+                int64_t max_pages) {
+  if (N < 0 || B < 0 || Hq < 1 || Hkv < 1 || D < 1 || num_pages < 1 || page_size < 1 ||
+      max_pages < 1 || Hq % Hkv != 0)
+    return W4V_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128 && D != 256) || page_size < 16 || page_size > 1024 ||
+      (page_size & (page_size - 1)) != 0 || B > kMaxGridYZ || max_pages > INT32_MAX ||
+      (int64_t)(Hq + 2ll * Hkv) * D > INT32_MAX)
+    return W4V_ERR_UNSUPPORTED;
+  return W4V_OK;
+}
+
+// bytes from the first to the last element of rows x width fp16 at row stride ld
+inline size_t span_f16(int rows, int64_t ld, int64_t width) {
+  return ((size_t)(rows - 1) * (size_t)ld + (size_t)width) * 2;
+}
+
+}  // namespace
+
+int rope_kv_append(const void* qkv, int64_t ldqkv, void* q_out, int64_t ldq, void* k_cache,
+                   void* v_cache, int num_pages, int page_size, const int32_t* block_table,
+                   int64_t max_pages, const int32_t* cu, const int32_t* ctx_lens,
+                   const float* inv_freq, float mscale, int N, int B, int Hq, int Hkv, int D,
+                   int rot, int interleaved, void* stream) {
+  int st = paged_sizes(N, B, Hq, Hkv, D, num_pages, page_size, max_pages);
+  if (st != W4V_OK) return st;
+  if (rot < 0 || rot > D) return W4V_ERR_INVALID_ARG;
+  if (rot % 16 != 0) return W4V_ERR_UNSUPPORTED;
+  if (N == 0 || B == 0) return W4V_OK;
+  int shift;
+  size_t cbytes;
+  st = paged_check(k_cache, v_cache, num_pages, page_size, block_table, max_pages, cu, ctx_lens,
+                   Hq, Hkv, D, &shift, &cbytes);
+  if (st != W4V_OK) return st;
+  const int64_t width = (int64_t)(Hq + 2 * Hkv) * D, qwidth = (int64_t)Hq * D;
+  if (!qkv || !q_out || (rot > 0 && !inv_freq) || ldqkv < width || ldq < qwidth)
+    return W4V_ERR_INVALID_ARG;
+  if (!aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(inv_freq, 4) || ldqkv % 8 != 0 ||
+      ldq % 8 != 0)
+    return W4V_ERR_ALIGNMENT;
+  const size_t xb = span_f16(N, ldqkv, width), qb = span_f16(N, ldq, qwidth);
+  if (ranges_overlap(qkv, xb, q_out, qb) && !(q_out == qkv && (N == 1 || ldq == ldqkv)))
+    return W4V_ERR_INVALID_ARG;
+  if (ranges_overlap(k_cache, cbytes, v_cache, cbytes) || ranges_overlap(k_cache, cbytes, qkv, xb) ||
+      ranges_overlap(v_cache, cbytes, qkv, xb) || ranges_overlap(k_cache, cbytes, q_out, qb) ||
+      ranges_overlap(v_cache, cbytes, q_out, qb))
+    return W4V_ERR_INVALID_ARG;
+  w4v::RopeArgs a;
+  a.qkv = static_cast<const _Float16*>(qkv);
+  a.ldqkv = ldqkv;
+  a.q_out = static_cast<_Float16*>(q_out);
+  a.ldq = ldq;
+  a.k_cache = static_cast<_Float16*>(k_cache);
+  a.v_cache = static_cast<_Float16*>(v_cache);
+  a.table = block_table;
+  a.max_pages = max_pages;
+  a.cu = cu;
+  a.ctx = ctx_lens;
+  a.inv_freq = inv_freq;
+  a.mscale = mscale;
+  a.N = N; a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.D = D;
+  a.rot = rot; a.interleaved = interleaved != 0;
+  a.num_pages = num_pages; a.page_size = page_size; a.page_shift = shift;
+  const hipError_t e = w4v::launch_rope_append(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? W4V_OK : W4V_ERR_HIP;
+}
+
+size_t paged_attention_workspace_size(int B, int max_q, int max_ctx, int Hq, int Hkv, int D) {
+  if (B <= 0 || max_q <= 0 || max_ctx < 0 ||
+      paged_sizes(1, B, Hq, Hkv, D, 1, 16, 1) != W4V_OK)
+    return 0;
+  return w4v::plan_attention(B, max_q, max_ctx, Hq, Hkv, D).partial_bytes;
+}
+
+int paged_attention(const void* q, int64_t ldq, const void* k_cache, const void* v_cache,
+                    int num_pages, int page_size, const int32_t* block_table, int64_t max_pages,
+                    const int32_t* cu, const int32_t* ctx_lens, void* out, int64_t ldo, int N, int B,
+                    int max_q, int max_ctx, int Hq, int Hkv, int D, float scale, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  int st = paged_sizes(N, B, Hq, Hkv, D, num_pages, page_size, max_pages);
+  if (st != W4V_OK) return st;
+  if (max_q < 0 || max_ctx < 0 || !(scale > 0.f) || !(scale <= 3.4e38f)) return W4V_ERR_INVALID_ARG;
+  if (N == 0 || B == 0 || max_q == 0) return W4V_OK;
+  if ((int64_t)max_q * Hq > INT32_MAX) return W4V_ERR_UNSUPPORTED;
+  int shift;
+  size_t cbytes;
+  st = paged_check(k_cache, v_cache, num_pages, page_size, block_table, max_pages, cu, ctx_lens,
+                   Hq, Hkv, D, &shift, &cbytes);
+  if (st != W4V_OK) return st;
+  const int64_t width = (int64_t)Hq * D;
+  if (!q || !out || ldq < width || ldo < width) return W4V_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || ldq % 8 != 0 || ldo % 8 != 0) return W4V_ERR_ALIGNMENT;
+  const size_t qb = span_f16(N, ldq, width), ob = span_f16(N, ldo, width);
+  if (ranges_overlap(out, ob, q, qb) || ranges_overlap(out, ob, k_cache, cbytes) ||
+      ranges_overlap(out, ob, v_cache, cbytes))
+    return W4V_ERR_INVALID_ARG;
+  const w4v::AttnPlan p = w4v::plan_attention(B, max_q, max_ctx, Hq, Hkv, D);
+  if (p.row_tiles > kMaxGridYZ) return W4V_ERR_UNSUPPORTED;
+  if (p.partial_bytes > 0) {
+    if (!workspace || workspace_bytes < p.partial_bytes) return W4V_ERR_WORKSPACE;
+    if (!aligned(workspace, w4v::kWorkspaceAlign)) return W4V_ERR_ALIGNMENT;
+  }
+  w4v::AttnArgs a;
+  a.q = static_cast<const _Float16*>(q);
+  a.ldq = ldq;
+  a.k_cache = static_cast<const _Float16*>(k_cache);
+  a.v_cache = static_cast<const _Float16*>(v_cache);
+  a.table = block_table;
+  a.max_pages = max_pages;
+  a.cu = cu;
+  a.ctx = ctx_lens;
+  a.out = static_cast<_Float16*>(out);
+  a.ldo = ldo;
+  a.scale = scale;
+  a.N = N; a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.D = D;
+  a.num_pages = num_pages; a.page_size = page_size; a.page_shift = shift;
+  a.max_q = max_q;
+  const hipError_t e = w4v::launch_attention(a, p, static_cast<float*>(workspace),
+                                             static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? W4V_OK : W4V_ERR_HIP;
+}
+
 int ngram_draft(const int32_t* history, int64_t ld, const int32_t* lengths, int B, int n_max,
                 int n_min, int K, int32_t* drafts, void* stream) {
   if (B < 0 || ld < 1 || K < 1 || n_min < 1 || n_max < n_min) return W4V_ERR_INVALID_ARG;

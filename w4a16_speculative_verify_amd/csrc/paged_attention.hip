@@ -1,0 +1,429 @@
+// Attention of a chunk of new tokens over a paged key/value cache, gfx950.
+#include "w4v_device.h"
+#include "w4v_launch.h"
+
+#include <algorithm>
+
+namespace w4v {
+
+namespace {
+
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef __fp16 h16x4 __attribute__((ext_vector_type(4)));
+#define W4V_LDS __attribute__((address_space(3)))
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr uint32_t kRing = 128 * 1024;     // LDS: the waves' key/value rings, then the merge
+constexpr float kLazy = 8.0f;              // running maxima move once a score exceeds them by 2^8
+
+// keys per tile and tiles in flight of one wave's ring: 32 KiB per wave
+template <int D>
+struct Ring {
+  static constexpr int KT = D == 256 ? 16 : 32;
+  static constexpr int NG = KT / 16;                     // 16-key groups of a tile
+  static constexpr uint32_t kGroup = 16 * D * 2;         // bytes of one group's keys (or values)
+  static constexpr uint32_t kTile = 2 * NG * kGroup;
+  static constexpr int NS = kRing / kWaves / kTile;
+  static constexpr int kDma = D / 32;                    // DMA instructions per group
+  static constexpr int kPer = 2 * NG * kDma;             // and per tile
+};
+
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)(W4V_LDS const void*)p;
+}
+
+// Chunk (16 bytes) swizzles inside a group's rows, see the layout notes above.
+template <int D>
+__device__ __forceinline__ int swz_k(int r) {
+  return D == 64 ? (r >> 1) & 7 : r & 15;
+}
+template <int D>
+__device__ __forceinline__ int swz_v(int r) {
+  return D == 64 ? ((r >> 1) & 3) * 2 : (2 * r) & 15;
+}
+
+__device__ __forceinline__ u32x4s rsrc_of(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return u32x4s{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu)),
+                (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
+}
+
+// the larger (or the sum) of the four lanes that hold one column
+template <typename F>
+__device__ __forceinline__ float over_groups(float v, F f) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  const uint32_t a0 = a[0], a1 = a[1];
+  v = f(__builtin_bit_cast(float, a0), __builtin_bit_cast(float, a1));
+  const uint32_t w = __builtin_bit_cast(uint32_t, v);
+  const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+  const uint32_t b0 = b[0], b1 = b[1];
+  return f(__builtin_bit_cast(float, b0), __builtin_bit_cast(float, b1));
+}
+__device__ __forceinline__ float max_groups(float v) {
+  return over_groups(v, [](float x, float y) { return fmaxf(x, y); });
+}
+__device__ __forceinline__ float sum_groups(float v) {
+  return over_groups(v, [](float x, float y) { return x + y; });
+}
+
+// A sequence of the batch as the kernels see it; offsets from the device are
+// held inside the rows and the table, whatever they say.
+struct Seq {
+  int start, T;      // first row, rows (at most max_q)
+  int p0;            // position of the first row (negative: rows before position 0)
+  int len;           // tokens with a place in the table
+};
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
+  Seq s;
+  const int lo = min(max(a.cu[b], 0), a.N), hi = min(max(a.cu[b + 1], lo), a.N);
+  const int64_t room = a.max_pages * a.page_size;
+  const int ctx = a.ctx[b];
+  s.start = lo;
+  s.p0 = ctx - (hi - lo);
+  s.T = min(hi - lo, a.max_q);
+  s.len = (int)min((int64_t)max(ctx, 0), room);
+  return s;
+}
+
+template <int D, int RT>
+__global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, int splits,
+                                                                  float* __restrict__ part) {
+  using L = Ring<D>;
+  constexpr int R = 16 * RT, DT = D / 16, DS = D / 32, NG = L::NG;
+  __shared__ __attribute__((aligned(1024))) unsigned char s_ring[kRing];
+  __shared__ float s_m[kWaves][R], s_l[kWaves][R];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, grp = lane >> 4;
+  const int G = a.Hq / a.Hkv;
+  const int h = blockIdx.x % a.Hkv, split = blockIdx.x / a.Hkv;
+  const int tile = gridDim.y - 1 - blockIdx.y, b = blockIdx.z;
+  const Seq sq = seq_of(a, b);
+  const int row0 = tile * R, nrows = sq.T * G;
+  if (row0 >= nrows) return;
+  const int last = min(row0 + R, nrows) - 1;
+  const int end = max(min(sq.len, sq.p0 + last / G + 1), 0);   // keys any row of the block sees
+  const int nt = (end + L::KT - 1) / L::KT;
+  const int t_lo = (int)((int64_t)nt * split / splits);
+  const int t_hi = (int)((int64_t)nt * (split + 1) / splits);
+  const int all_see = sq.p0 + row0 / G;                        // keys up to here every row sees
+
+  f16x8 q[RT][DS];
+  int lim[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int x = min(row0 + 16 * rt + col, nrows - 1);
+    const int i = x / G, g = x % G;
+    lim[rt] = min(sq.p0 + i, sq.len - 1);
+    const _Float16* p = a.q + (int64_t)(sq.start + i) * a.ldq + (h * G + g) * D + 8 * grp;
+#pragma unroll
+    for (int s = 0; s < DS; ++s) q[rt][s] = *reinterpret_cast<const f16x8*>(p + 32 * s);
+  }
+
+  // DMA source offsets of this lane inside a group: LDS chunk position -> chunk
+  uint32_t ko[L::kDma], vo[L::kDma];
+#pragma unroll
+  for (int u = 0; u < L::kDma; ++u) {
+    const int at = u * 64 + lane, r = at / (D / 8), c = at % (D / 8);
+    ko[u] = (uint32_t)(r * D * 2 + (c ^ swz_k<D>(r)) * 16);
+    vo[u] = (uint32_t)(r * D * 2 + (c ^ swz_v<D>(r)) * 16);
+  }
+  const uint32_t ring = lds_addr(s_ring) + wave * (kRing / kWaves);
+  const int32_t* table = a.table + (int64_t)b * a.max_pages;
+
+  // page of group gi of tile t (-1 behind the end)
+  const auto page_of = [&](int t, int gi) -> int {
+    const int key = t * L::KT + 16 * gi;
+    if (t >= t_hi || key >= end) return -1;
+    const int p = table[key >> a.page_shift];
+    return (unsigned)p < (unsigned)a.num_pages ? p : -1;
+  };
+  const auto issue = [&](int t, int slot, const int* pages) {
+#pragma unroll
+    for (int gi = 0; gi < NG; ++gi) {
+      const int key = t * L::KT + 16 * gi;
+      const int pg = pages[gi];
+      const int64_t off =
+          pg < 0 ? 0 : (((int64_t)pg * a.Hkv + h) * a.page_size + (key & (a.page_size - 1))) * D;
+      const uint32_t bytes = pg < 0 ? 0u : (uint32_t)min(16, end - key) * (D * 2);
+      const u32x4s rk = rsrc_of(a.k_cache + off, bytes), rv = rsrc_of(a.v_cache + off, bytes);
+      const uint32_t dst = ring + slot * L::kTile + gi * L::kGroup;
+#pragma unroll
+      for (int u = 0; u < L::kDma; ++u) {
+        dma16(dst + u * 1024, rk, ko[u]);
+        dma16(dst + NG * L::kGroup + u * 1024, rv, vo[u]);
+      }
+    }
+  };
+
+  f32x4 o[RT][DT];
+  float m[RT], l[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    m[rt] = -INFINITY;
+    l[rt] = 0.f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[rt][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  int pg[L::NS][NG], pn[NG];
+  const int t0 = t_lo + wave;
+#pragma unroll
+  for (int s = 0; s < L::NS; ++s) {
+#pragma unroll
+    for (int gi = 0; gi < NG; ++gi) pg[s][gi] = page_of(t0 + s * kWaves, gi);
+    issue(t0 + s * kWaves, s, pg[s]);
+  }
+#pragma unroll
+  for (int gi = 0; gi < NG; ++gi) pn[gi] = page_of(t0 + L::NS * kWaves, gi);
+
+  const float c = a.scale * 1.44269504088896341f;
+  // lane offsets of the operand reads
+  uint32_t ka[DS];
+#pragma unroll
+  for (int s = 0; s < DS; ++s)
+    ka[s] = (uint32_t)(col * D * 2 + ((4 * s + grp) ^ swz_k<D>(col)) * 16);
+  const int vkey = 4 * grp + col / 4;
+  uint32_t va[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+    va[d] = (uint32_t)(vkey * D * 2 + ((2 * d + (col & 3) / 2) ^ swz_v<D>(vkey)) * 16 + (col & 1) * 8);
+
+  int slot = 0;
+  for (int t = t0; t < t_hi; t += kWaves) {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((L::NS - 1) * L::kPer) : "memory");
+    const uint32_t kb = ring + slot * L::kTile, vb = kb + NG * L::kGroup;
+
+    f32x4 sc[RT][NG];
+#pragma unroll
+    for (int gi = 0; gi < NG; ++gi) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) sc[rt][gi] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < DS; ++s) {
+        const f16x8 k = *(W4V_LDS f16x8*)(kb + gi * L::kGroup + ka[s]);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) sc[rt][gi] = mfma16x16x32(k, q[rt][s], sc[rt][gi]);
+      }
+    }
+    bool hide = t * L::KT + L::KT - 1 > all_see;
+#pragma unroll
+    for (int gi = 0; gi < NG; ++gi) hide |= pg[0][gi] < 0;
+
+    f16x8 p[RT];
+    f16x4 p4[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float v = sc[rt][gi][r] * c;
+          if (hide) {
+            const int key = t * L::KT + 16 * gi + 4 * grp + r;
+            v = key <= lim[rt] && pg[0][gi] >= 0 ? v : -INFINITY;
+          }
+          sc[rt][gi][r] = v;
+          mx = fmaxf(mx, v);
+        }
+      mx = max_groups(mx);
+      if (__any(mx > m[rt] + kLazy)) {
+        const float mn = fmaxf(m[rt], mx);
+        const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[rt] - mn);
+        m[rt] = mn;
+        l[rt] *= f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[rt][d][r] *= f;
+      }
+      const float mu = m[rt] == -INFINITY ? 0.f : m[rt];
+#pragma unroll
+      for (int gi = 0; gi < NG; ++gi)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float e = __builtin_amdgcn_exp2f(sc[rt][gi][r] - mu);
+          l[rt] += e;
+          if constexpr (NG == 2) p[rt][4 * gi + r] = (_Float16)e;
+          else p4[rt][r] = (_Float16)e;
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      const h16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4f16((W4V_LDS h16x4*)(vb + va[d]));
+      if constexpr (NG == 2) {
+        const h16x4 v1 =
+            __builtin_amdgcn_ds_read_tr16_b64_v4f16((W4V_LDS h16x4*)(vb + L::kGroup + va[d]));
+        f16x8 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          v[r] = (_Float16)v0[r];
+          v[4 + r] = (_Float16)v1[r];
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) o[rt][d] = mfma16x16x32(v, p[rt], o[rt][d]);
+      } else {
+        f16x4 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = (_Float16)v0[r];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          o[rt][d] = __builtin_amdgcn_mfma_f32_16x16x16f16(v, p4[rt], o[rt][d], 0, 0, 0);
+      }
+    }
+    // the slot's reads are done: refill it
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    issue(t + L::NS * kWaves, slot, pn);
+#pragma unroll
+    for (int s = 0; s + 1 < L::NS; ++s)
+#pragma unroll
+      for (int gi = 0; gi < NG; ++gi) pg[s][gi] = pg[s + 1][gi];
+#pragma unroll
+    for (int gi = 0; gi < NG; ++gi) {
+      pg[L::NS - 1][gi] = pn[gi];
+      pn[gi] = page_of(t + (L::NS + 1) * kWaves, gi);
+    }
+    slot = slot + 1 == L::NS ? 0 : slot + 1;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy lands in the ring any more
+  __syncthreads();
+
+  // ---- the waves' sums are joined through LDS
+  float* so = reinterpret_cast<float*>(s_ring);      // [wave][row][D], chunks of 4 swizzled by row
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    l[rt] = sum_groups(l[rt]);
+    const int r = 16 * rt + col;
+    if (grp == 0) {
+      s_m[wave][r] = m[rt];
+      s_l[wave][r] = l[rt];
+    }
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+      *reinterpret_cast<f32x4*>(so + ((wave * R + r) * D + (((4 * d + grp) ^ col) * 4))) = o[rt][d];
+  }
+  __syncthreads();
+  for (int i = tid; i < R * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), ch = i % (D / 4), x = row0 + r;
+    if (x >= nrows) break;
+    float mx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, s_m[w][r]);
+    const float mu = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f;
+    f32x4 acc{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float f = __builtin_amdgcn_exp2f(s_m[w][r] - mu);
+      const f32x4 v =
+          *reinterpret_cast<const f32x4*>(so + ((w * R + r) * D + ((ch ^ (r & 15)) * 4)));
+      sum += f * s_l[w][r];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(f, v[e], acc[e]);
+    }
+    if (splits == 1) {
+      const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+      f16x4 y;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = (_Float16)(acc[e] * inv);
+      *reinterpret_cast<f16x4*>(a.out + (int64_t)(sq.start + x / G) * a.ldo + (h * G + x % G) * D +
+                                4 * ch) = y;
+    } else {
+      const int64_t item = (((int64_t)b * a.Hkv + h) * gridDim.y + tile) * splits + split;
+      float* po = part + item * R * (D + 2);
+      *reinterpret_cast<f32x4*>(po + (int64_t)r * D + 4 * ch) = acc;
+      if (ch == 0) {
+        po[(int64_t)R * D + 2 * r] = mx;
+        po[(int64_t)R * D + 2 * r + 1] = sum;
+      }
+    }
+  }
+}
+
+// Joins the splits of one (token, query head) per wave.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int splits, int row_tiles, int R,
+                                                        const float* __restrict__ part) {
+  constexpr int PL = D / 64;
+  const int lane = threadIdx.x & 63;
+  const int y = blockIdx.x * 4 + (threadIdx.x >> 6), b = blockIdx.y;
+  const Seq sq = seq_of(a, b);
+  const int G = a.Hq / a.Hkv;
+  const int i = y / a.Hq, head = y % a.Hq;
+  if (i >= sq.T) return;
+  const int h = head / G, x = i * G + head % G, tile = x / R, r = x % R;
+  const float* base = part + (((int64_t)b * a.Hkv + h) * row_tiles + tile) * splits * R * (D + 2);
+  const int64_t step = (int64_t)R * (D + 2);
+  float ms = -INFINITY, ls = 0.f;
+  if (lane < splits) {
+    ms = base[lane * step + R * D + 2 * r];
+    ls = base[lane * step + R * D + 2 * r + 1];
+  }
+  float mx = ms;
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) mx = fmaxf(mx, __shfl_xor(mx, k, 64));
+  const float f = ms == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms - mx);
+  float sum = f * ls;
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) sum += __shfl_xor(sum, k, 64);
+  float acc[PL];
+#pragma unroll
+  for (int e = 0; e < PL; ++e) acc[e] = 0.f;
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    const float w = __shfl(f, s, 64);
+    const float* p = base + s * step + (int64_t)r * D + lane * PL;
+#pragma unroll
+    for (int e = 0; e < PL; ++e) acc[e] = __builtin_fmaf(w, p[e], acc[e]);
+  }
+  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+  _Float16* out = a.out + (int64_t)(sq.start + i) * a.ldo + (int64_t)head * D + lane * PL;
+#pragma unroll
+  for (int e = 0; e < PL; ++e) out[e] = (_Float16)(acc[e] * inv);
+}
+
+template <int D, int RT>
+void launch_stream(const AttnArgs& a, const AttnPlan& p, float* partials, hipStream_t stream) {
+  hipLaunchKernelGGL((attn_stream_kernel<D, RT>), dim3(a.Hkv * p.splits, p.row_tiles, a.B),
+                     dim3(kThreads), 0, stream, a, p.splits, partials);
+  if (p.splits > 1)
+    hipLaunchKernelGGL(attn_join_kernel<D>, dim3((a.max_q * a.Hq + 3) / 4, a.B), dim3(256), 0,
+                       stream, a, p.splits, p.row_tiles, p.rows, partials);
+}
+
+template <int D>
+void launch_d(const AttnArgs& a, const AttnPlan& p, float* partials, hipStream_t stream) {
+  if (p.rows == 16) launch_stream<D, 1>(a, p, partials, stream);
+  else if (p.rows == 32) launch_stream<D, 2>(a, p, partials, stream);
+  else if constexpr (D != 256) launch_stream<D, 4>(a, p, partials, stream);
+}
+
+}  // namespace
+
+AttnPlan plan_attention(int B, int max_q, int max_ctx, int Hq, int Hkv, int D) {
+  AttnPlan p;
+  const int64_t rows = (int64_t)max_q * (Hq / Hkv);
+  p.rows = rows <= 16 ? 16 : (rows <= 32 || D == 256 ? 32 : 64);
+  p.row_tiles = (int)((rows + p.rows - 1) / p.rows);
+  const int64_t items = (int64_t)B * Hkv * p.row_tiles;
+  const int tiles = (max_ctx + 31) / 32;
+  p.splits = 1;
+  if (items < 256) p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({64, 256 / items, tiles / 8}));
+  p.partial_bytes = p.splits == 1 ? 0 : (size_t)items * p.splits * p.rows * (D + 2) * sizeof(float);
+  return p;
+}
+
+hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, float* partials,
+                            hipStream_t stream) {
+  if (a.D == 64) launch_d<64>(a, p, partials, stream);
+  else if (a.D == 128) launch_d<128>(a, p, partials, stream);
+  else launch_d<256>(a, p, partials, stream);
+  return hipGetLastError();
+}
+
+}  // namespace w4v

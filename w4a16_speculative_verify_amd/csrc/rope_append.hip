@@ -1,0 +1,149 @@
+// Rotary positions and the append to a paged key/value cache, gfx950: the step
+// between the fused QKV linear and the attention of a verify block or a prompt
+// chunk ("Efficient LLM Challenge Results", section 3: the target's forward
+// pass over the K + 1 positions).
+//
+// Row r of sequence b sits at position p = ctx_b - cu_{b+1} + r.  Its query and
+// key heads are rotated pair by pair,
+//   (x0, x1) -> m (x0 cos t - x1 sin t, x1 cos t + x0 sin t),  t = p f_j,
+// the pair being elements (j, j + rot/2) or (2j, 2j + 1) of the head, the rest
+// of the head copied; the query goes to q_out, the rotated key and the value to
+// the row's slot of the cache, page table[b][p / page_size].
+//
+// The angle is formed in 64 bits and reduced to a fraction of a turn there: at
+// p = 1e6 the 32-bit product p f_j alone would be off by 0.03 rad.  The table
+// f_j is the caller's, so every scaling for long contexts is one table.
+//
+// Bound by the bytes of qkv, read once and written once.  One block per row:
+// the rot/2 angles are computed once per row, by one thread each, and shared by
+// all heads through LDS; each thread then moves 32-byte items (two 16-byte
+// chunks that hold 8 whole pairs), whose loads are issued before the angles are
+// computed.
+#include "w4v_device.h"
+#include "w4v_launch.h"
+
+namespace w4v {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxHalf = 128;              // rot / 2 at the widest head (256)
+constexpr int kItems = 2;                  // items per thread whose loads go out ahead of the angles
+
+// chunks (16 bytes) an item covers, and whether it is rotated
+struct Item {
+  int head, c0, c1;
+  bool rot;
+};
+
+__device__ __forceinline__ Item item_of(int i, const RopeArgs& a) {
+  const int per = a.D / 16;                // items per head
+  Item t;
+  t.head = i / per;
+  const int u = i % per;
+  t.rot = t.head < a.Hq + a.Hkv && u < a.rot / 16;
+  if (t.rot && !a.interleaved) {
+    t.c0 = u;
+    t.c1 = u + a.rot / 16;
+  } else {
+    t.c0 = 2 * u;
+    t.c1 = 2 * u + 1;
+  }
+  return t;
+}
+
+__global__ __launch_bounds__(kThreads) void rope_append_kernel(RopeArgs a) {
+  __shared__ float s_cos[kMaxHalf], s_sin[kMaxHalf];
+  const int row = blockIdx.x;
+  const int tid = threadIdx.x;
+  const int n_items = (a.Hq + 2 * a.Hkv) * (a.D / 16);
+  const _Float16* src = a.qkv + (int64_t)row * a.ldqkv;
+
+  // the first items' loads do not depend on the position: they go out first
+  f16x8 lo[kItems], hi[kItems];
+#pragma unroll
+  for (int u = 0; u < kItems; ++u) {
+    const int i = tid + u * kThreads;
+    if (i < n_items) {
+      const Item t = item_of(i, a);
+      lo[u] = *reinterpret_cast<const f16x8*>(src + t.head * a.D + t.c0 * 8);
+      hi[u] = *reinterpret_cast<const f16x8*>(src + t.head * a.D + t.c1 * 8);
+    }
+  }
+
+  const RowPlace w = place_of_row(a.cu, a.ctx, a.B, row);
+  if (w.seq < 0 || w.pos < 0) return;      // behind the last sequence, or before position 0
+
+  const int half = a.rot / 2;
+  if (tid < half) {
+    const double turns = (double)w.pos * (double)a.inv_freq[tid] * 0.15915494309189533577;
+    float sn, cs;
+    sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cs);
+    s_cos[tid] = cs * a.mscale;
+    s_sin[tid] = sn * a.mscale;
+  }
+  const int pidx = w.pos >> a.page_shift;
+  int page = -1;
+  if (pidx < a.max_pages) page = a.table[(int64_t)w.seq * a.max_pages + pidx];
+  const bool stored = page >= 0 && page < a.num_pages;
+  // element offset of the row's slot for key/value head 0; head h adds h * head_stride
+  const int64_t head_stride = (int64_t)a.page_size * a.D;
+  const int64_t slot = stored ? ((int64_t)page * a.Hkv * a.page_size + (w.pos & (a.page_size - 1))) * a.D : 0;
+  __syncthreads();
+
+  const auto one = [&](int i, f16x8 x, f16x8 y) {
+    const Item t = item_of(i, a);
+    if (t.rot) {
+      if (!a.interleaved) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float c = s_cos[t.c0 * 8 + e], s = s_sin[t.c0 * 8 + e];
+          const float p = (float)x[e], q = (float)y[e];
+          x[e] = (_Float16)(p * c - q * s);
+          y[e] = (_Float16)(q * c + p * s);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const int j = t.c0 * 4 + e / 2;
+          const float c = s_cos[j], s = s_sin[j], c2 = s_cos[j + 4], s2 = s_sin[j + 4];
+          const float p = (float)x[e], q = (float)x[e + 1];
+          x[e] = (_Float16)(p * c - q * s);
+          x[e + 1] = (_Float16)(q * c + p * s);
+          const float p2 = (float)y[e], q2 = (float)y[e + 1];
+          y[e] = (_Float16)(p2 * c2 - q2 * s2);
+          y[e + 1] = (_Float16)(q2 * c2 + p2 * s2);
+        }
+      }
+    }
+    _Float16* dst;
+    if (t.head < a.Hq) {
+      dst = a.q_out + (int64_t)row * a.ldq + t.head * a.D;
+    } else {
+      if (!stored) return;
+      const int h = t.head - a.Hq;
+      dst = (h < a.Hkv ? a.k_cache + h * head_stride : a.v_cache + (h - a.Hkv) * head_stride) + slot;
+    }
+    *reinterpret_cast<f16x8*>(dst + t.c0 * 8) = x;
+    *reinterpret_cast<f16x8*>(dst + t.c1 * 8) = y;
+  };
+#pragma unroll
+  for (int u = 0; u < kItems; ++u) {
+    const int i = tid + u * kThreads;
+    if (i < n_items) one(i, lo[u], hi[u]);
+  }
+  for (int i = tid + kItems * kThreads; i < n_items; i += kThreads) {
+    const Item t = item_of(i, a);
+    one(i, *reinterpret_cast<const f16x8*>(src + t.head * a.D + t.c0 * 8),
+        *reinterpret_cast<const f16x8*>(src + t.head * a.D + t.c1 * 8));
+  }
+}
+
+}  // namespace
+
+hipError_t launch_rope_append(const RopeArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL(rope_append_kernel, dim3(a.N), dim3(kThreads), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace w4v

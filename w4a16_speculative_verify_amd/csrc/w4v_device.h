@@ -252,6 +252,26 @@ __device__ __forceinline__ void dma4(uint32_t lds_addr, u32x4s src, uint32_t off
 // 8 consecutive rows of one chunk in distinct banks for the writes.
 __device__ __forceinline__ int lds_sw4(int r) { return (4 - ((r >> 2) & 3)) & 3; }
 
+// Where a row of a ragged batch belongs: rows cu[b] .. cu[b + 1] - 1 are the
+// newest tokens of sequence b, whose ctx[b] tokens include them.  A row behind
+// cu[B] belongs to none (seq -1).  Every wave counts the sequences that end at
+// or before the row, 64 at a time, so one load round serves 64 sequences.
+struct RowPlace {
+  int seq, pos;
+};
+__device__ __forceinline__ RowPlace place_of_row(const int32_t* cu, const int32_t* ctx, int B,
+                                                 int row) {
+  const int lane = threadIdx.x & 63;
+  int seq = 0;
+  for (int b0 = 0; b0 < B; b0 += 64) {
+    const bool past = b0 + lane < B && cu[b0 + lane + 1] <= row;
+    seq += __popcll(__ballot(past));
+  }
+  seq = __builtin_amdgcn_readfirstlane(seq);
+  if (seq >= B || row < cu[0]) return RowPlace{-1, -1};
+  return RowPlace{seq, ctx[seq] - cu[seq + 1] + row};
+}
+
 // Total order for greedy argmax: larger value first, then lower index.
 __device__ __forceinline__ bool better(float v, int i, float bv, int bi) {
   return v > bv || (v == bv && i < bi);

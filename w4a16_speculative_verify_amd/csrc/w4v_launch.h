@@ -208,6 +208,44 @@ hipError_t launch_gdn_commit(float* state, const float* k, const float* v, const
                              const float* beta, const int32_t* accepted_len, int B, int T, int H,
                              int D, hipStream_t stream);
 
+// ---------------------------------------------------------------- attention
+// Rows of a ragged batch: sequence b has rows cu[b] .. cu[b + 1] - 1, the newest
+// of its ctx[b] tokens; cache page table[b][p / page_size] holds its position p.
+// Caches are [num_pages][Hkv][page_size][D].
+struct RopeArgs {
+  const _Float16* qkv; int64_t ldqkv;
+  _Float16* q_out; int64_t ldq;
+  _Float16* k_cache; _Float16* v_cache;
+  const int32_t* table; int64_t max_pages;
+  const int32_t* cu; const int32_t* ctx;
+  const float* inv_freq;
+  float mscale;
+  int N, B, Hq, Hkv, D, rot, interleaved, num_pages, page_size, page_shift;
+};
+hipError_t launch_rope_append(const RopeArgs& a, hipStream_t stream);
+
+struct AttnArgs {
+  const _Float16* q; int64_t ldq;
+  const _Float16* k_cache; const _Float16* v_cache;
+  const int32_t* table; int64_t max_pages;
+  const int32_t* cu; const int32_t* ctx;
+  _Float16* out; int64_t ldo;
+  float scale;
+  int N, B, Hq, Hkv, D, num_pages, page_size, page_shift, max_q;   // page_size = 1 << page_shift
+};
+
+// Packed rows: the G = Hq / Hkv query heads of one key/value head share its keys,
+// so row x of a (sequence, head) is query token x / G, head x % G.
+struct AttnPlan {
+  int rows;            // packed rows a block takes
+  int row_tiles;       // blocks along the packed rows of the longest sequence
+  int splits;          // blocks along the context (1 = none)
+  size_t partial_bytes;
+};
+AttnPlan plan_attention(int B, int max_q, int max_ctx, int Hq, int Hkv, int D);
+hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, float* partials,
+                            hipStream_t stream);
+
 // ---------------------------------------------------------------- verify
 // HBM read-bandwidth probe: kReadProbeBlocks blocks, one XOR word each in out
 constexpr int kReadProbeBlocks = 2048;
