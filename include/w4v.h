@@ -292,6 +292,43 @@ int gdn_state_commit(float* state, const float* k, const float* v, const float* 
                      void* stream);
 
 /* ------------------------------------------------------------------------
+ * The gated delta rule of a Gated DeltaNet layer (hazards list: most of the
+ * target's layers are Gated DeltaNet): outputs of every position and, where
+ * asked for, the state after the last one.
+ *   S <- alpha_t * S (I - beta_t k_t k_t^T) + beta_t v_t k_t^T;   o_t = scale * S q_t
+ * With state_out NULL it is the verify's form: the K + 1 positions are scored and
+ * the state stays as committed; gdn_state_commit then advances it by the accepted
+ * prefix.
+ * Batch    rows cu[b] .. cu[b+1]-1 (int32 [B+1], ascending, read on the device) are
+ *          the positions of sequence b, in order; a sequence without rows keeps
+ *          its state (state_out gets a copy).  Rows of no sequence are left as
+ *          they were.
+ * q, k     [N x Hk D], v [N x H D], o [N x H D] out: fp16 (f32 == 0) or fp32
+ *          (f32 != 0), row strides ldq, ldk, ldv, ldo in elements; 16-byte aligned,
+ *          strides multiples of 8.  H a multiple of Hk: head h reads key head
+ *          h / (H / Hk).  Keys have unit length in the layer; any values are taken.
+ * alpha, beta  fp32 [N x H]: decay gate and write strength.
+ * state    fp32 [B x H x D x D] (S[b, h] is [dv x dk] row-major), 16-byte aligned;
+ *          state_out the same, equal to state (in place), disjoint from it, or NULL.
+ *          o and state_out overlap no input (o not q, k, v; state aside).
+ * Sizes    D 64 or 128 (W4V_ERR_UNSUPPORTED otherwise); B, H <= 65535.
+ * max_t    the most rows a sequence has: chooses the form (the results stay right
+ *          whatever it is).  fp16 inputs with max_t above 64 take the chunked form: 64
+ *          positions at a time on the matrix cores, the state in fp32, every operand
+ *          that is not fp16 already as an exact pair of fp16 (22 bits); entries of the
+ *          state, or of beta (v - S k), at or past 65,504 overflow there.  Otherwise
+ *          positions are taken one by one in fp32.
+ * workspace  gdn_forward_workspace_size(...) bytes of scratch (0 for the recurrent
+ *          form), 256-byte aligned, no contents expected or kept.
+ * ---------------------------------------------------------------------- */
+size_t gdn_forward_workspace_size(int N, int B, int max_t, int Hk, int H, int D, int f32);
+
+int gdn_forward(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                const float* alpha, const float* beta, const int32_t* cu, const float* state,
+                float* state_out, void* o, int64_t ldo, int N, int B, int max_t, int Hk, int H,
+                int D, int f32, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Attention of the target's layers over the verify block (section 3: the
  * target's forward pass over the K + 1 positions) or a chunk of a prompt, on a
  * paged key/value cache: rope_kv_append rotates the new queries and keys and

@@ -48,3 +48,27 @@ def commit(state, k, v, alpha, beta, accepted_len) -> np.ndarray:
                 S = gdn_update(S, k[b, t, h], v[b, t, h], float(alpha[b, t, h]), float(beta[b, t, h]))
             out[b, h] = S
     return out
+
+
+def forward(q, k, v, alpha, beta, cu, state, scale: float):
+    """(o fp64 [N, H, dv] with NaN in rows of no sequence, state fp64 [B, H, dv, dk] after the last
+    rows): o_t = scale * S_t q_t over the rows cu[b] .. cu[b+1]-1 of every sequence.
+
+    q, k [N, Hk, dk]; v [N, H, dv]; head h reads key head h // (H // Hk); alpha, beta [N, H].
+    """
+    state = np.asarray(state, np.float64)
+    v = np.asarray(v, np.float64)
+    H = v.shape[1]
+    g = H // np.asarray(k).shape[1]
+    out = state.copy()
+    o = np.full(v.shape, np.nan)
+    for b in range(len(cu) - 1):
+        for h in range(H):
+            S = out[b, h]
+            for t in range(int(cu[b]), int(cu[b + 1])):
+                kt = np.asarray(k[t, h // g], np.float64)
+                a, be = float(alpha[t, h]), float(beta[t, h])
+                S = a * (S - be * np.outer(S @ kt, kt)) + be * np.outer(v[t, h], kt)
+                o[t, h] = scale * (S @ np.asarray(q[t, h // g], np.float64))
+            out[b, h] = S
+    return o, out

@@ -448,3 +448,47 @@ def test_rope_frequency_tables():
     for bad in (dict(rot=3), dict(rot=-2), dict(rot=8, factor=0.0), dict(rot=8, scaling="cubic")):
         with pytest.raises(ValueError):
             w4v.rope_inv_freq(device="cpu", **bad)
+
+
+# ------------------------------------------------------------------ gated delta rule
+def gdn(lib, q=G, ldq=2048, k=2 * G, ldk=2048, v=3 * G, ldv=2048, al=4 * G, be=5 * G, cu=A, s=6 * G,
+        so=7 * G, o=8 * G, ldo=2048, N=100, B=2, max_t=50, Hk=16, H=16, D=128, f32=0, scale=0.1, ws=A,
+        wsb=1 << 40):
+    return lib.gdn_forward(q, ldq, k, ldk, v, ldv, al, be, cu, s, so, o, ldo, N, B, max_t, Hk, H, D, f32,
+                           ctypes.c_float(scale), ws, wsb, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(B=0), OK), (dict(N=0, so=None), OK), (dict(N=0, so=6 * G), OK),
+    (dict(N=-1), INVALID), (dict(B=-1), INVALID), (dict(max_t=-1), INVALID), (dict(Hk=0), INVALID),
+    (dict(Hk=3), INVALID), (dict(D=96), UNSUPPORTED), (dict(D=256), UNSUPPORTED),
+    (dict(B=70000), UNSUPPORTED), (dict(Hk=1, H=70000, ldv=70000 * 128), UNSUPPORTED),
+    (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
+    (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(al=None), INVALID),
+    (dict(be=None), INVALID), (dict(cu=None), INVALID), (dict(s=None), INVALID), (dict(o=None), INVALID),
+    (dict(ldq=2040), INVALID), (dict(ldk=2040), INVALID), (dict(ldv=2040), INVALID),
+    (dict(ldo=2040), INVALID), (dict(ldq=2052), ALIGN), (dict(ldo=2052), ALIGN),
+    (dict(q=G + 8), ALIGN), (dict(o=8 * G + 8), ALIGN), (dict(s=6 * G + 8), ALIGN),
+    (dict(so=7 * G + 4), ALIGN), (dict(al=4 * G + 2), ALIGN), (dict(cu=A + 2), ALIGN),
+    (dict(o=G), INVALID), (dict(o=3 * G), INVALID), (dict(o=6 * G + 1024), INVALID),
+    (dict(so=6 * G + 4096), INVALID),                # partly the state
+    (dict(so=3 * G), INVALID), (dict(so=5 * G), INVALID), (dict(so=8 * G), INVALID),
+    (dict(o=2 * G - 8192, f32=1), INVALID),          # fp32 rows are twice as long
+    (dict(max_t=65, ws=None, wsb=0), WORKSPACE),
+])
+def test_gdn_forward_validation(lib, kw, status):
+    assert gdn(lib, **kw) == status
+
+
+def test_gdn_forward_workspace(lib):
+    import torch
+    size = w4v.gdn_forward_workspace_size
+    assert size(100, 2, 64, 16, 16, 128, torch.float16) == 0      # position by position
+    assert size(8192, 1, 8192, 16, 16, 128, torch.float32) == 0
+    need = size(8192, 1, 8192, 16, 16, 128, torch.float16)
+    assert need > 0 and need == size(8192, 1, 65, 16, 16, 64, torch.float16)
+    assert size(0, 2, 100, 16, 16, 128, torch.float16) == 0
+    assert size(100, 2, 100, 16, 16, 96, torch.float16) == 0
+    need = size(100, 2, 100, 16, 16, 128, torch.float16)
+    assert gdn(lib, max_t=100, wsb=need - 1) == WORKSPACE
+    assert gdn(lib, max_t=100, ws=A + 16) == ALIGN

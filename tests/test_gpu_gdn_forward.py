@@ -1,0 +1,274 @@
+"""GPU parity of the gated delta rule's outputs and state against the fp64
+oracle, in both forms.
+
+Tolerances.  A step adds to the state a relative error of at most about
+sqrt(D) 2^-23 (a D-term fp32 dot product and a rank-one update, the bound
+gdn_state_commit is held to); with unit keys, |alpha| <= 1 and beta <= 1 a step
+does not enlarge what is there, so n remembered steps give n sqrt(D) 2^-23.  A
+chunk of 64 positions makes its products from pairs of fp16 whose remainder is
+2^-22 of each operand, three such products in a row, so it is off by less than
+its 64 steps would be.  Gates drawn from [0.9, 1) remember about 20 steps: 32
+steps, 5e-5 at D = 128, as for the commit.  Without decay n is the length.  The
+state is compared by relative L2 per head (and 10 times that elementwise,
+against the rms).  Outputs: the same relative error of the output vector's
+length, 10 times that elementwise, plus for fp16 the rounding of the result,
+2^-11 of it (2^-25 where subnormal).
+"""
+import numpy as np
+import pytest
+
+import gen
+from oracle import gdn
+from tests.gpu_util import dev, host, log
+
+pytestmark = pytest.mark.gpu
+
+
+def inputs(rng, new, hk, h, d, dtype, pad=0):
+    """(q, k, v, alpha, beta, cu, state) of a ragged batch, drawn as gen.gdn_inputs draws a block's."""
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    n = int(cu[-1]) + pad
+    S, k, v, al, be = gen.gdn_inputs(rng, 1, max(n, 1), h, d, d)
+    q = rng.standard_normal((n, hk, d))
+    q = q / np.linalg.norm(q, axis=-1, keepdims=True)
+    state = rng.standard_normal((len(new), h, d, d)).astype(np.float32)
+    return (q.astype(dtype), np.ascontiguousarray(k[0, :n, :hk]).astype(dtype), v[0, :n].astype(dtype),
+            al[0, :n].copy(), be[0, :n].copy(), cu, state)
+
+
+def check(x, o, s, steps=32, scale=None, what=""):
+    q, k, v, al, be, cu, state = x
+    d = v.shape[-1]
+    scale = d ** -0.5 if scale is None else scale
+    ro, rs = gdn.forward(q, k, v, al, be, cu, state, scale)
+    tol = max(5e-5, steps * np.sqrt(d) * 2.0**-23)
+    worst = 0.0
+    live = ~np.isnan(ro[:, 0, 0])
+    if live.any():
+        g, r = np.asarray(o, np.float64)[live], ro[live]
+        assert np.all(np.isfinite(g)), what
+        # the output's size where nothing cancels: |S_t| |q|, at least the output itself
+        size = np.sqrt(np.mean(r * r, axis=-1, keepdims=True)) + 1e-30
+        size = np.maximum(size, np.median(size, axis=0, keepdims=True))
+        rnd = (2.0**-11 * np.abs(r) + 2.0**-25) if v.dtype == np.float16 else 0.0
+        worst = np.max(np.abs(g - r) / (10 * tol * size + rnd))
+        assert worst <= 1.0, f"{what} outputs: {worst:.2f} of the tolerance"
+    if s is not None:
+        s = np.asarray(s, np.float64)
+        assert np.all(np.isfinite(s)), what
+        for i in np.ndindex(rs.shape[:2]):
+            norm = np.linalg.norm(rs[i])
+            rel = np.linalg.norm(s[i] - rs[i]) / norm
+            mx = np.max(np.abs(s[i] - rs[i])) / (norm / d)
+            assert rel <= tol and mx <= 10 * tol, f"{what} state {i}: rel-L2 {rel:.2e}, max/rms {mx:.2e}"
+            worst = max(worst, rel / tol)
+    return worst
+
+
+def run(lib, x, max_t=None, steps=32, scale=None, what="", in_place=False, update=True):
+    import torch
+    q, k, v, al, be, cu, state = x
+    t = int(np.max(np.diff(cu))) if max_t is None else max_t
+    s = dev(state)
+    so = (s if in_place else torch.full_like(s, 5.0)) if update else None
+    out = torch.full(v.shape, 3.0, dtype=torch.float16 if v.dtype == np.float16 else torch.float32,
+                     device="cuda")
+    lib.gdn_forward(dev(q), dev(k), dev(v), dev(al), dev(be), dev(cu), s, t, state_out=so, scale=scale,
+                    out=out)
+    torch.cuda.synchronize()
+    if not in_place:
+        assert np.array_equal(host(s), state)
+    o = host(out)
+    assert np.all(o[int(cu[-1]):] == 3.0) and np.all(o[:int(cu[0])] == 3.0)
+    w = check(x, o, host(so) if update else None, steps, scale, what)
+    return o, (host(so) if update else None), w
+
+
+@pytest.mark.parametrize("new,hk,h,d,dtype", [
+    ([1], 2, 2, 128, np.float32),
+    ([1, 1, 1], 2, 6, 64, np.float16),
+    ([16, 3, 0, 17], 4, 4, 128, np.float16),                  # a verify block, a sequence without rows
+    ([33, 15, 32], 1, 3, 64, np.float32),
+    ([64], 2, 4, 128, np.float16),                            # the longest recurrent fp16 block
+    ([65], 2, 4, 128, np.float16),                            # the shortest chunked one
+    ([128, 127, 129, 1, 0, 63], 2, 2, 64, np.float16),
+    ([200, 64, 70], 1, 4, 128, np.float16),
+    ([700], 2, 2, 128, np.float16),
+    ([300, 90], 2, 2, 128, np.float32),                       # fp32: position by position
+])
+def test_forward_matches_oracle(lib, new, hk, h, d, dtype):
+    rng = np.random.default_rng(sum(new) + h + d)
+    x = inputs(rng, new, hk, h, d, dtype, pad=5)
+    _, _, w = run(lib, x, what=f"{new}")
+    log(f"  {new} {hk}/{h} d={d}: {w:.2f} of the tolerance")
+
+
+@pytest.mark.parametrize("max_t", [1, 64, 65, 100000])
+def test_the_hint_shapes_the_launch_only(lib, max_t):
+    """Any max_t gives the result, in either form; sequences in place."""
+    rng = np.random.default_rng(max_t)
+    x = inputs(rng, [130, 1, 0, 77], 2, 2, 64, np.float16, pad=1)
+    run(lib, x, max_t=max_t, in_place=True, what=f"max_t {max_t}")
+
+
+def test_without_a_state_to_write(lib):
+    rng = np.random.default_rng(20)
+    for new in ([21] * 3, [90, 150]):
+        x = inputs(rng, new, 2, 4, 128, np.float16)
+        a, _, _ = run(lib, x, update=False)
+        b, _, _ = run(lib, x)
+        assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [np.float16, np.float32])
+def test_no_rows_at_all(lib, dtype):
+    import torch
+    rng = np.random.default_rng(21)
+    x = inputs(rng, [0, 0], 1, 2, 64, dtype)
+    _, s, _ = run(lib, x, max_t=0)
+    assert np.array_equal(s, x[6])
+    x = inputs(rng, [0, 0], 1, 2, 64, dtype, pad=70)
+    _, s, _ = run(lib, x, max_t=70)
+    assert np.array_equal(s, x[6])
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("new", [[40], [180]])
+@pytest.mark.parametrize("case", ["reset", "keep", "repeat", "long_memory", "closed", "negative"])
+def test_gates_at_their_ends(lib, new, case):
+    """Decay gates of zero (the state starts anew) and one, full writes of one key over and over
+    (the triangular system's worst conditioning), write strength zero, and a negative decay."""
+    rng = np.random.default_rng(22)
+    q, k, v, al, be, cu, s = inputs(rng, new, 2, 2, 128, np.float16)
+    steps = 32
+    if case == "reset":
+        al[[0, 7, 30, new[0] - 1]] = 0.0
+    elif case == "keep":
+        al[:] = 1.0
+        steps = new[0]
+    elif case == "repeat":
+        k[:] = k[:1]
+        al[:], be[:] = 1.0, 1.0
+        steps = new[0]
+    elif case == "long_memory":
+        al[:] = np.float32(1 - 2.0**-12)
+        be[:] = 1.0
+        steps = new[0]
+    elif case == "closed":
+        be[:] = 0.0
+    else:
+        al[::3] *= -1
+    run(lib, (q, k, v, al, be, cu, s), steps=steps, what=case)
+
+
+def test_tiny_decay_products(lib):
+    """Gates whose product leaves the range of fp32 inside a chunk: what is forgotten is zero, never
+    a quotient of zeros."""
+    rng = np.random.default_rng(23)
+    x = inputs(rng, [150], 1, 2, 64, np.float16)
+    x[3][:] = np.float32(1e-3)
+    run(lib, x)
+
+
+def test_rows_of_others_may_hold_anything(lib):
+    """NaN in the rows behind a sequence that ends inside a chunk, and in a neighbour's."""
+    rng = np.random.default_rng(24)
+    q, k, v, al, be, cu, s = inputs(rng, [70, 100, 30], 2, 2, 128, np.float16, pad=9)
+    clean, cs, _ = run(lib, (q, k, v, al, be, cu, s), max_t=100)
+    for a in (q, k, v, al, be):
+        a[70:170] = np.nan
+        a[200:] = np.inf
+    s[1] = np.nan
+    import torch
+    out = torch.zeros(v.shape, dtype=torch.float16, device="cuda")
+    so = torch.zeros(s.shape, dtype=torch.float32, device="cuda")
+    for max_t in (100, 1):
+        lib.gdn_forward(dev(q), dev(k), dev(v), dev(al), dev(be), dev(cu), dev(s), max_t, state_out=so,
+                        out=out)
+        torch.cuda.synchronize()
+        if max_t == 100:
+            assert np.array_equal(host(out)[:70], clean[:70])
+            assert np.array_equal(host(out)[170:200], clean[170:200])
+            assert np.array_equal(host(so)[[0, 2]], cs[[0, 2]])
+        else:
+            assert np.all(np.isfinite(host(out)[:70])) and np.all(np.isfinite(host(so)[[0, 2]]))
+
+
+def test_strided_rows(lib):
+    """q, k, v as columns of one fused projection, out as columns of a wider buffer."""
+    import torch
+    rng = np.random.default_rng(25)
+    for new in ([9, 20], [100, 70]):
+        q, k, v, al, be, cu, s = inputs(rng, new, 2, 4, 64, np.float16)
+        n = len(q)
+        want, ws, _ = run(lib, (q, k, v, al, be, cu, s))
+        wide = torch.full((n, 8 * 64 + 40), float("nan"), dtype=torch.float16, device="cuda")
+        wide[:, :128] = dev(q).view(n, -1)
+        wide[:, 128:256] = dev(k).view(n, -1)
+        wide[:, 256:512] = dev(v).view(n, -1)
+        o = torch.full((n, 4 * 64 + 64), 5.0, dtype=torch.float16, device="cuda")
+        sd = dev(s)
+        lib.gdn_forward(wide[:, :128].view(n, 2, 64), wide[:, 128:256].view(n, 2, 64),
+                        wide[:, 256:512].view(n, 4, 64), dev(al), dev(be), dev(cu), sd, max(new),
+                        state_out=sd, out=o[:, 32:288].view(n, 4, 64))
+        torch.cuda.synchronize()
+        assert np.array_equal(host(o)[:, 32:288].reshape(n, 4, 64), want)
+        assert np.all(host(o)[:, :32] == 5) and np.all(host(o)[:, 288:] == 5)
+        assert np.array_equal(host(sd), ws)
+
+
+def test_verify_block_then_commit(lib):
+    """The verify's use: outputs of the whole block with the state left alone, then the commit of
+    the accepted prefix, against the forward over that prefix alone."""
+    import torch
+    rng = np.random.default_rng(26)
+    B, K1, H, D = 3, 16, 4, 128
+    for step in range(3):
+        x = inputs(rng, [K1] * B, H, H, D, np.float32)
+        q, k, v, al, be, cu, s = x
+        run(lib, x, update=False)
+        acc = rng.integers(0, K1, B).astype(np.int32)
+        sd = dev(s)
+        shape = (B, K1, H)
+        lib.gdn_state_commit(sd, dev(k.reshape(*shape, D)), dev(v.reshape(*shape, D)),
+                             dev(al.reshape(shape)), dev(be.reshape(shape)), dev(acc))
+        keep = np.concatenate([np.arange(b * K1, b * K1 + acc[b] + 1) for b in range(B)])
+        cu2 = np.concatenate([[0], np.cumsum(acc + 1)]).astype(np.int32)
+        y = (q[keep], k[keep], v[keep], al[keep], be[keep], cu2, s)
+        _, s2, _ = run(lib, y)
+        torch.cuda.synchronize()
+        assert np.linalg.norm(host(sd) - s2) <= 1e-4 * np.linalg.norm(s2)
+
+
+@pytest.mark.parametrize("new", [[5, 12], [100, 30]])
+def test_captured_and_on_another_stream(lib, new):
+    """A captured call (state in place) replayed with eager work between equals the eager call each
+    time; a call on another stream gives the same bits."""
+    import torch
+    rng = np.random.default_rng(27)
+    q, k, v, al, be, cu, s = (dev(a) for a in inputs(rng, new, 2, 2, 128, np.float16))
+    t = max(new)
+    ws = lib.new_workspace(lib.gdn_forward_workspace_size(len(q), 2, t, 2, 2, 128, q.dtype))
+    o, sd = torch.empty_like(v), s.clone()
+    lib.gdn_forward(q, k, v, al, be, cu, sd, t, state_out=sd, out=o, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lib.gdn_forward(q, k, v, al, be, cu, sd, t, state_out=sd, out=o, workspace=ws)
+    for rep in range(3):
+        sd.copy_(s * (rep + 1))
+        se = s * (rep + 1)
+        for _ in range(2):
+            v.copy_(torch.roll(v, 1, 0))
+            g.replay()
+            torch.cuda.synchronize()
+            oe = lib.gdn_forward(q, k, v, al, be, cu, se, t, state_out=se)
+            torch.cuda.synchronize()
+            assert torch.equal(oe, o) and torch.equal(se, sd)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    s1, s2 = torch.empty_like(s), torch.empty_like(s)
+    a = lib.gdn_forward(q, k, v, al, be, cu, s, t, state_out=s1, stream=st)
+    b = lib.gdn_forward(q, k, v, al, be, cu, s, t, state_out=s2)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b) and torch.equal(s1, s2)

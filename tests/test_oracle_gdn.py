@@ -83,3 +83,36 @@ def test_exact_rationals_tiny_state():
         M = [[a * (M[i][j] - b * Sk[i] * kk[j]) + b * vv[i] * kk[j] for j in range(dk)]
              for i in range(dv)]
     assert np.array_equal(out, np.array([[float(x) for x in row] for row in M]))
+
+
+def test_forward_is_the_update_read_by_the_query():
+    """forward against gdn_update step by step, ragged sequences and shared key heads; its state
+    against commit with every position accepted."""
+    rng = np.random.default_rng(5)
+    cu, H, Hk, D = [0, 3, 3, 7], 4, 2, 6
+    q, k = rng.standard_normal((2, 9, Hk, D))
+    v = rng.standard_normal((9, H, D))
+    al, be = rng.uniform(0.5, 1, (9, H)), rng.uniform(0, 1, (9, H))
+    S0 = rng.standard_normal((3, H, D, D))
+    o, S = gdn.forward(q, k, v, al, be, cu, S0, 0.5)
+    for b in range(3):
+        for h in range(H):
+            X = S0[b, h]
+            for t in range(cu[b], cu[b + 1]):
+                X = gdn.gdn_update(X, k[t, h // 2], v[t, h], al[t, h], be[t, h])
+                assert np.allclose(o[t, h], 0.5 * X @ q[t, h // 2], rtol=1e-12, atol=1e-12)
+            assert np.allclose(S[b, h], X, rtol=1e-12, atol=1e-12)
+    assert np.all(np.isnan(o[7:])) and np.array_equal(S[1], S0[1])
+    kk = np.repeat(k[None, :3], 2, axis=2)
+    c = gdn.commit(S0[:1], kk, v[None, :3], al[None, :3], be[None, :3], [2])
+    assert np.allclose(c[0], S[0], rtol=1e-12, atol=1e-12)
+
+
+def test_forward_reads_back_what_a_full_write_stored():
+    """beta = 1, alpha = 1, orthonormal keys: the query equal to a key reads that key's value."""
+    D = 8
+    k = np.eye(D)[:, None, :]
+    v = np.arange(D * D, dtype=float).reshape(D, 1, D)
+    one = np.ones((D, 1))
+    o, S = gdn.forward(k, k, v, one, one, [0, D], np.full((1, 1, D, D), 9.0), 2.0)
+    assert np.array_equal(o[:, 0], 2 * v[:, 0]) and np.array_equal(S[0, 0], v[:, 0].T)

@@ -56,6 +56,9 @@ SIGNATURES = {
     "f16_lmhead_argmax_verify": (_int, [_vp, _i64, _vp, _vp, _vp, _int, _int, _int, _vp, _int,
                                         _int, _vp, _vp, _vp, _sz, _vp]),
     "gdn_state_commit": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _int, _int, _int, _int, _vp]),
+    "gdn_forward_workspace_size": (_sz, [_int] * 7),
+    "gdn_forward": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _int,
+                           _int, _int, _int, _int, _int, _int, ctypes.c_float, _vp, _sz, _vp]),
     "rope_kv_append": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _int, _int, _vp, _i64, _vp, _vp, _vp,
                               ctypes.c_float, _int, _int, _int, _int, _int, _int, _int, _vp]),
     "paged_attention_workspace_size": (_sz, [_int] * 6),
@@ -562,8 +565,7 @@ def rope_kv_append(qkv, k_cache, v_cache, block_table, cu, ctx_lens, inv_freq, h
     if q_out is None:
         q_out = torch.empty((n, hq, d), dtype=torch.float16, device=qkv.device)
     _require(q_out, torch.float16, "q_out")
-    if q_out.shape[0] != n or q_out.numel() != n * hq * d or \
-            (q_out.dim() == 3 and q_out.stride(1) != d and q_out.shape[1] > 1):
+    if q_out.shape[0] != n or q_out.numel() != n * hq * d or not _heads_contiguous(q_out):
         raise ValueError(f"q_out must be [{n}, {hq}, {d}] or [{n}, {hq * d}], heads contiguous")
     _on_device(qkv.device, k_cache=k_cache, v_cache=v_cache, block_table=block_table, cu=cu,
                ctx_lens=ctx_lens, inv_freq=inv_freq, q_out=q_out)
@@ -575,6 +577,12 @@ def rope_kv_append(qkv, k_cache, v_cache, block_table, cu, ctx_lens, inv_freq, h
         ctypes.c_float(mscale), n, b, hq, hkv, d, 2 * inv_freq.numel(), int(interleaved), _stream())
     _check(st, "rope_kv_append")
     return q_out
+
+
+def _heads_contiguous(t):
+    """Whether a row's heads follow each other: [N, heads * D], or [N, heads, D] with that stride."""
+    return t.dim() == 2 or (t.dim() == 3 and (t.shape[1] < 2 or t.numel() == 0 or
+                                              t.stride(1) == t.shape[2]))
 
 
 def _ld(t, width):
@@ -605,14 +613,13 @@ def paged_attention(q, k_cache, v_cache, block_table, cu, ctx_lens, max_q: int, 
                                    scale, out, workspace)
     torch = _require(q, __import__("torch").float16, "q")
     pages, hkv, page, d, b = _paged(k_cache, v_cache, block_table, cu, ctx_lens)
-    if q.dim() != 3 or q.shape[2] != d or (q.shape[1] > 1 and q.stride(1) != d):
+    if q.dim() != 3 or q.shape[2] != d or not _heads_contiguous(q):
         raise ValueError(f"q must be [N, heads, {d}], heads contiguous, got {tuple(q.shape)}")
     n, hq = q.shape[0], q.shape[1]
     if out is None:
         out = torch.empty((n, hq, d), dtype=torch.float16, device=q.device)
     _require(out, torch.float16, "out")
-    if out.shape[0] != n or out.numel() != n * hq * d or \
-            (out.dim() == 3 and out.stride(1) != d and hq > 1):
+    if out.shape[0] != n or out.numel() != n * hq * d or not _heads_contiguous(out):
         raise ValueError(f"out must be [{n}, {hq}, {d}] or [{n}, {hq * d}], heads contiguous")
     if max_ctx is None:
         max_ctx = min(block_table.shape[1] * page, 2**31 - 1)
@@ -628,6 +635,70 @@ def paged_attention(q, k_cache, v_cache, block_table, cu, ctx_lens, max_q: int, 
         hq, hkv, d, ctypes.c_float(d ** -0.5 if scale is None else scale), _ptr(workspace), wbytes,
         _stream())
     _check(st, "paged_attention")
+    return out
+
+
+# ------------------------------------------------------------------- gated delta rule
+def gdn_forward_workspace_size(n: int, b: int, max_t: int, hk: int, h: int, d: int, dtype) -> int:
+    import torch
+    return int(load().gdn_forward_workspace_size(n, b, max_t, hk, h, d,
+                                                 int(dtype == torch.float32)))
+
+
+def gdn_forward(q, k, v, alpha, beta, cu, state, max_t: int, state_out=None, scale=None, out=None,
+                workspace=None, stream=None):
+    """Outputs o[N, H, D] = scale * S_t q_t of the gated delta rule over ragged sequences.
+
+    q, k [N, Hk, D], v [N, H, D], all fp16 or all fp32 (rows may be strided, heads contiguous);
+    alpha, beta fp32 [N, H]; cu int32 [B + 1]: sequence b's rows; state fp32 [B, H, D, D], the
+    states before them.  ``state_out`` (state itself, or another such tensor) takes the states
+    after the last rows; without it the state is left alone (the verify's form, see
+    gdn_state_commit).  ``max_t``: the most rows a sequence has; ``scale`` D^-0.5 by default.
+    Returns out (q's dtype); rows of no sequence are not written.
+    """
+    if _elsewhere(q, stream):
+        import torch
+        with torch.cuda.device(q.device), torch.cuda.stream(stream):
+            return gdn_forward(q, k, v, alpha, beta, cu, state, max_t, state_out, scale, out, workspace)
+    import torch
+    dt = q.dtype
+    if dt not in (torch.float16, torch.float32):
+        raise ValueError(f"q must be float16 or float32, got {dt}")
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        _require(t, dt, name)
+        if t.dim() != 3 or not _heads_contiguous(t):
+            raise ValueError(f"{name} must be [N, heads, D], heads contiguous")
+    n, hk, d = q.shape
+    h = v.shape[1]
+    b = cu.shape[0] - 1
+    if k.shape != q.shape or tuple(v.shape) != (n, h, d) or tuple(state.shape) != (b, h, d, d) or \
+            tuple(alpha.shape) != (n, h) or tuple(beta.shape) != (n, h):
+        raise ValueError("gdn_forward: shapes do not match q [N, Hk, D], v [N, H, D], state [B, H, D, D]")
+    _require(cu, torch.int32, "cu")
+    for t, name in ((alpha, "alpha"), (beta, "beta"), (state, "state"), (state_out, "state_out")):
+        if t is not None:
+            _require(t, torch.float32, name)
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+    if state_out is not None and state_out.shape != state.shape:
+        raise ValueError("state_out must have state's shape")
+    if out is None:
+        out = torch.empty((n, h, d), dtype=dt, device=q.device)
+    _require(out, dt, "out")
+    if out.shape[0] != n or out.numel() != n * h * d or not _heads_contiguous(out):
+        raise ValueError(f"out must be [{n}, {h}, {d}] or [{n}, {h * d}], heads contiguous")
+    need = gdn_forward_workspace_size(n, b, max_t, hk, h, d, dt)
+    if workspace is None and need > 0:
+        workspace = new_workspace(need, q.device)
+    _on_device(q.device, k=k, v=v, alpha=alpha, beta=beta, cu=cu, state=state, state_out=state_out,
+               out=out, workspace=workspace)
+    wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = load().gdn_forward(
+        _ptr(q), _ld(q, hk * d), _ptr(k), _ld(k, hk * d), _ptr(v), _ld(v, h * d), _ptr(alpha),
+        _ptr(beta), _ptr(cu), _ptr(state), _ptr(state_out), _ptr(out), _ld(out, h * d), n, b, max_t,
+        hk, h, d, int(dt == torch.float32), ctypes.c_float(d ** -0.5 if scale is None else scale),
+        _ptr(workspace), wbytes, _stream())
+    _check(st, "gdn_forward")
     return out
 
 

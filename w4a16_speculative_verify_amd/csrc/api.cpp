@@ -688,10 +688,8 @@ int paged_attention(const void* q, int64_t ldq, const void* k_cache, const void*
     return W4V_ERR_INVALID_ARG;
   const w4v::AttnPlan p = w4v::plan_attention(B, max_q, max_ctx, Hq, Hkv, D);
   if (p.row_tiles > kMaxGridYZ) return W4V_ERR_UNSUPPORTED;
-  if (p.partial_bytes > 0) {
-    if (!workspace || workspace_bytes < p.partial_bytes) return W4V_ERR_WORKSPACE;
-    if (!aligned(workspace, w4v::kWorkspaceAlign)) return W4V_ERR_ALIGNMENT;
-  }
+  st = workspace_check(p.partial_bytes, workspace, workspace_bytes);
+  if (st != W4V_OK) return st;
   w4v::AttnArgs a;
   a.q = static_cast<const _Float16*>(q);
   a.ldq = ldq;
@@ -709,6 +707,75 @@ int paged_attention(const void* q, int64_t ldq, const void* k_cache, const void*
   a.max_q = max_q;
   const hipError_t e = w4v::launch_attention(a, p, static_cast<float*>(workspace),
                                              static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? W4V_OK : W4V_ERR_HIP;
+}
+
+namespace {
+
+int gdn_sizes(int N, int B, int max_t, int Hk, int H, int D) {
+  if (N < 0 || B < 0 || max_t < 0 || Hk < 1 || H < 1 || D < 1 || H % Hk != 0)
+    return W4V_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || B > kMaxGridYZ || H > kMaxGridYZ) return W4V_ERR_UNSUPPORTED;
+  return W4V_OK;
+}
+
+}  // namespace
+
+size_t gdn_forward_workspace_size(int N, int B, int max_t, int Hk, int H, int D, int f32) {
+  if (gdn_sizes(N, B, max_t, Hk, H, D) != W4V_OK || N == 0 || B == 0) return 0;
+  return w4v::gdn_forward_workspace(w4v::plan_gdn(N, max_t, f32), N, B, H);
+}
+
+int gdn_forward(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                const float* alpha, const float* beta, const int32_t* cu, const float* state,
+                float* state_out, void* o, int64_t ldo, int N, int B, int max_t, int Hk, int H,
+                int D, int f32, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = gdn_sizes(N, B, max_t, Hk, H, D);
+  if (st != W4V_OK) return st;
+  if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return W4V_ERR_INVALID_ARG;
+  if (B == 0 || (N == 0 && (!state_out || state_out == state))) return W4V_OK;
+  if (!cu || !state) return W4V_ERR_INVALID_ARG;
+  if (!aligned(cu, 4) || !aligned(state, 16) || !aligned(state_out, 16)) return W4V_ERR_ALIGNMENT;
+  const size_t sbytes = (size_t)B * H * D * D * 4;
+  if (state_out && state_out != state && ranges_overlap(state, sbytes, state_out, sbytes))
+    return W4V_ERR_INVALID_ARG;
+  if (N > 0) {
+    const int64_t kw = (int64_t)Hk * D, vw = (int64_t)H * D;
+    if (!q || !k || !v || !alpha || !beta || !o || ldq < kw || ldk < kw || ldv < vw || ldo < vw)
+      return W4V_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) ||
+        !aligned(alpha, 4) || !aligned(beta, 4) || ldq % 8 != 0 || ldk % 8 != 0 || ldv % 8 != 0 ||
+        ldo % 8 != 0)
+      return W4V_ERR_ALIGNMENT;
+    const int es = f32 ? 2 : 1;            // fp16 spans per element
+    const size_t gb = (size_t)N * H * 4;
+    const struct { const void* p; size_t n; } in[] = {
+        {q, span_f16(N, ldq, kw) * es}, {k, span_f16(N, ldk, kw) * es},
+        {v, span_f16(N, ldv, vw) * es}, {alpha, gb}, {beta, gb}, {state, sbytes}};
+    const size_t ob = span_f16(N, ldo, vw) * es;
+    for (const auto& x : in) {
+      if (ranges_overlap(o, ob, x.p, x.n)) return W4V_ERR_INVALID_ARG;
+      if (state_out && x.p != state && ranges_overlap(state_out, sbytes, x.p, x.n))
+        return W4V_ERR_INVALID_ARG;
+    }
+    if (state_out && ranges_overlap(state_out, sbytes, o, ob)) return W4V_ERR_INVALID_ARG;
+  }
+  const w4v::GdnPlan p = w4v::plan_gdn(N, max_t, f32);
+  st = workspace_check(w4v::gdn_forward_workspace(p, N, B, H), workspace, workspace_bytes);
+  if (st != W4V_OK) return st;
+  w4v::GdnArgs a;
+  a.q = q; a.ldq = ldq;
+  a.k = k; a.ldk = ldk;
+  a.v = v; a.ldv = ldv;
+  a.alpha = alpha;
+  a.beta = beta;
+  a.cu = cu;
+  a.state = state;
+  a.state_out = state_out;
+  a.o = o; a.ldo = ldo;
+  a.scale = scale;
+  a.N = N; a.B = B; a.Hk = Hk; a.H = H; a.D = D; a.f32 = f32 != 0;
+  const hipError_t e = w4v::launch_gdn_forward(a, p, workspace, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? W4V_OK : W4V_ERR_HIP;
 }
 

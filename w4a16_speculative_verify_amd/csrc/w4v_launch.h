@@ -208,6 +208,26 @@ hipError_t launch_gdn_commit(float* state, const float* k, const float* v, const
                              const float* beta, const int32_t* accepted_len, int B, int T, int H,
                              int D, hipStream_t stream);
 
+// The layer's outputs and state over a ragged batch (rows cu[b] .. cu[b + 1] - 1)
+constexpr int kGdnChunk = 64;     // tokens the chunked form takes at a time
+struct GdnArgs {
+  const void* q; int64_t ldq;
+  const void* k; int64_t ldk;
+  const void* v; int64_t ldv;
+  const float* alpha; const float* beta;
+  const int32_t* cu;
+  const float* state; float* state_out;    // state_out may be state, or NULL
+  void* o; int64_t ldo;
+  float scale;
+  int N, B, Hk, H, D, f32;
+};
+struct GdnPlan {
+  bool chunked;
+};
+GdnPlan plan_gdn(int N, int max_t, int f32);
+size_t gdn_forward_workspace(const GdnPlan& p, int N, int B, int H);
+hipError_t launch_gdn_forward(const GdnArgs& a, const GdnPlan& p, void* ws, hipStream_t stream);
+
 // ---------------------------------------------------------------- attention
 // Rows of a ragged batch: sequence b has rows cu[b] .. cu[b + 1] - 1, the newest
 // of its ctx[b] tokens; cache page table[b][p / page_size] holds its position p.
