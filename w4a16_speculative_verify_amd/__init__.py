@@ -130,6 +130,12 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _raw_stream(device):
+    """The current stream of a device as an integer, without building a Stream object (2.7 us)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else None
 
@@ -470,39 +476,79 @@ class Chain:
 
 
 # ------------------------------------------------------------------- attention
+# The calls below are often the only work of a few microseconds on the GPU, so
+# their checks touch every tensor once and build no objects on the way.
 def _elsewhere(t, stream):
     """Whether a call has to enter another device or stream first (its own allocations then belong
     to that stream)."""
     import torch
-    if stream is not None and stream.device != t.device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
-    return stream is not None or t.device.index != torch.cuda.current_device()
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+        return True
+    return t.is_cuda and t.device.index != torch.cuda.current_device()
 
 
-def _on_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
+def _whole(t, dtype, device, name):
+    """A contiguous tensor of this type on this device."""
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _require(t, dtype, name)
+        if t.device != device:
             raise ValueError(f"{name} is on {t.device}, not on {device}")
+        raise ValueError(f"{name} must be contiguous")
 
 
-def _paged(k_cache, v_cache, block_table, cu, ctx_lens):
+def _rows(t, dtype, device, name, n, heads, d):
+    """[n, heads, d] (or [n, heads * d]) of this type on this device, a row's heads contiguous, rows
+    at any stride; returns the row stride (the width for a single row, whose stride says nothing)."""
+    if t.dtype is not dtype or t.device != device:
+        _require(t, dtype, name)
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        ok = shape == (n, heads, d) and (n == 0 or (stride[2] == 1 and
+                                                    (heads == 1 or stride[1] == d)))
+    else:
+        ok = shape == (n, heads * d) and (n == 0 or stride[1] == 1)
+    if not ok:
+        raise ValueError(f"{name} must be [{n}, {heads}, {d}] or [{n}, {heads * d}], heads contiguous, "
+                         f"got {tuple(shape)} with strides {stride}")
+    return stride[0] if n > 1 else heads * d
+
+
+def _paged(k_cache, v_cache, block_table, cu, ctx_lens, device):
     """(pages, kv heads, page size, head width, sequences) of a paged cache and its batch."""
-    torch = _require(k_cache, __import__("torch").float16, "k_cache")
-    _require(v_cache, torch.float16, "v_cache")
-    for t, name in ((block_table, "block_table"), (cu, "cu"), (ctx_lens, "ctx_lens")):
-        _require(t, torch.int32, name)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    import torch
+    _whole(k_cache, torch.float16, device, "k_cache")
+    _whole(v_cache, torch.float16, device, "v_cache")
+    _whole(block_table, torch.int32, device, "block_table")
+    _whole(cu, torch.int32, device, "cu")
+    _whole(ctx_lens, torch.int32, device, "ctx_lens")
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must both be [pages, kv heads, page size, D]")
-    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
-        raise ValueError("k_cache and v_cache must be contiguous")
+    if ctx_lens.dim() != 1:
+        raise ValueError("ctx_lens must be [B]")
     b = ctx_lens.shape[0]
-    if ctx_lens.dim() != 1 or tuple(cu.shape) != (b + 1,):
+    if cu.shape != (b + 1,):
         raise ValueError("cu must have one entry more than ctx_lens")
     if block_table.dim() != 2 or block_table.shape[0] != b:
         raise ValueError("block_table must be [B, max_pages]")
-    return (*k_cache.shape, b)
+    return (*shape, b)
+
+
+def _scratch(workspace, need, device):
+    """(pointer, bytes, the tensor that holds it) of a call's workspace, allocated where none is given."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        import torch
+        workspace = torch.empty(need + 256, dtype=torch.uint8, device=device)
+        off = -workspace.data_ptr() % 256
+        return workspace.data_ptr() + off, need, workspace
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def rope_inv_freq(rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -551,44 +597,30 @@ def rope_kv_append(qkv, k_cache, v_cache, block_table, cu, ctx_lens, inv_freq, h
     (rope_inv_freq).  Returns q_out fp16 [N, hq, D] (``q_out`` may be qkv[:, :hq * D] itself);
     rows that belong to no sequence or lie before position 0 are not written.
     """
+    import torch
     if _elsewhere(qkv, stream):
-        import torch
         with torch.cuda.device(qkv.device), torch.cuda.stream(stream):
             return rope_kv_append(qkv, k_cache, v_cache, block_table, cu, ctx_lens, inv_freq, hq,
                                   interleaved, mscale, q_out)
-    torch = _require(qkv, __import__("torch").float16, "qkv")
-    pages, hkv, page, d, b = _paged(k_cache, v_cache, block_table, cu, ctx_lens)
-    _require(inv_freq, torch.float32, "inv_freq")
-    if qkv.dim() != 2 or qkv.shape[1] < (hq + 2 * hkv) * d:
-        raise ValueError(f"qkv must be [N, >= {(hq + 2 * hkv) * d}], got {tuple(qkv.shape)}")
+    dev = qkv.device
+    _require(qkv, torch.float16, "qkv")
+    pages, hkv, page, d, b = _paged(k_cache, v_cache, block_table, cu, ctx_lens, dev)
+    _whole(inv_freq, torch.float32, dev, "inv_freq")
+    width = (hq + 2 * hkv) * d
+    if qkv.dim() != 2 or qkv.shape[1] < width:
+        raise ValueError(f"qkv must be [N, >= {width}], got {tuple(qkv.shape)}")
     n = qkv.shape[0]
     if q_out is None:
-        q_out = torch.empty((n, hq, d), dtype=torch.float16, device=qkv.device)
-    _require(q_out, torch.float16, "q_out")
-    if q_out.shape[0] != n or q_out.numel() != n * hq * d or not _heads_contiguous(q_out):
-        raise ValueError(f"q_out must be [{n}, {hq}, {d}] or [{n}, {hq * d}], heads contiguous")
-    _on_device(qkv.device, k_cache=k_cache, v_cache=v_cache, block_table=block_table, cu=cu,
-               ctx_lens=ctx_lens, inv_freq=inv_freq, q_out=q_out)
-    if not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be contiguous")
+        q_out = torch.empty((n, hq, d), dtype=torch.float16, device=dev)
+    ldq = _rows(q_out, torch.float16, dev, "q_out", n, hq, d)
     st = load().rope_kv_append(
-        _ptr(qkv), _ld(qkv, (hq + 2 * hkv) * d), _ptr(q_out), _ld(q_out, hq * d), _ptr(k_cache),
-        _ptr(v_cache), pages, page, _ptr(block_table), block_table.shape[1], _ptr(cu), _ptr(ctx_lens), _ptr(inv_freq),
-        ctypes.c_float(mscale), n, b, hq, hkv, d, 2 * inv_freq.numel(), int(interleaved), _stream())
-    _check(st, "rope_kv_append")
+        qkv.data_ptr(), qkv.stride(0) if n > 1 else width, q_out.data_ptr(), ldq,
+        k_cache.data_ptr(), v_cache.data_ptr(), pages, page, block_table.data_ptr(),
+        block_table.shape[1], cu.data_ptr(), ctx_lens.data_ptr(), inv_freq.data_ptr(), mscale, n, b,
+        hq, hkv, d, 2 * inv_freq.numel(), interleaved, _raw_stream(dev))
+    if st:
+        _check(st, "rope_kv_append")
     return q_out
-
-
-def _heads_contiguous(t):
-    """Whether a row's heads follow each other: [N, heads * D], or [N, heads, D] with that stride."""
-    return t.dim() == 2 or (t.dim() == 3 and (t.shape[1] < 2 or t.numel() == 0 or
-                                              t.stride(1) == t.shape[2]))
-
-
-def _ld(t, width):
-    """Row stride of a tensor whose rows are its first dimension (the width for a single row, whose
-    stride says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else width
 
 
 def paged_attention_workspace_size(b: int, max_q: int, max_ctx: int, hq: int, hkv: int,
@@ -606,35 +638,33 @@ def paged_attention(q, k_cache, v_cache, block_table, cu, ctx_lens, max_q: int, 
     rows may be strided.  Returns out fp16 [N, hq, D]; rows that see no token are zeros, rows
     behind the last sequence are not written.
     """
+    import torch
     if _elsewhere(q, stream):
-        import torch
         with torch.cuda.device(q.device), torch.cuda.stream(stream):
             return paged_attention(q, k_cache, v_cache, block_table, cu, ctx_lens, max_q, max_ctx,
                                    scale, out, workspace)
-    torch = _require(q, __import__("torch").float16, "q")
-    pages, hkv, page, d, b = _paged(k_cache, v_cache, block_table, cu, ctx_lens)
-    if q.dim() != 3 or q.shape[2] != d or not _heads_contiguous(q):
-        raise ValueError(f"q must be [N, heads, {d}], heads contiguous, got {tuple(q.shape)}")
+    dev = q.device
+    pages, hkv, page, d, b = _paged(k_cache, v_cache, block_table, cu, ctx_lens, dev)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [N, heads, D], got {tuple(q.shape)}")
     n, hq = q.shape[0], q.shape[1]
+    ldq = _rows(q, torch.float16, dev, "q", n, hq, d)
     if out is None:
-        out = torch.empty((n, hq, d), dtype=torch.float16, device=q.device)
-    _require(out, torch.float16, "out")
-    if out.shape[0] != n or out.numel() != n * hq * d or not _heads_contiguous(out):
-        raise ValueError(f"out must be [{n}, {hq}, {d}] or [{n}, {hq * d}], heads contiguous")
+        out = torch.empty((n, hq, d), dtype=torch.float16, device=dev)
+    ldo = _rows(out, torch.float16, dev, "out", n, hq, d)
     if max_ctx is None:
         max_ctx = min(block_table.shape[1] * page, 2**31 - 1)
-    need = paged_attention_workspace_size(b, max_q, max_ctx, hq, hkv, d)
-    if workspace is None and need > 0:
-        workspace = new_workspace(need, q.device)
-    _on_device(q.device, k_cache=k_cache, v_cache=v_cache, block_table=block_table, cu=cu,
-               ctx_lens=ctx_lens, out=out, workspace=workspace)
-    wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    st = load().paged_attention(
-        _ptr(q), _ld(q, hq * d), _ptr(k_cache), _ptr(v_cache), pages, page, _ptr(block_table),
-        block_table.shape[1], _ptr(cu), _ptr(ctx_lens), _ptr(out), _ld(out, hq * d), n, b, max_q, max_ctx,
-        hq, hkv, d, ctypes.c_float(d ** -0.5 if scale is None else scale), _ptr(workspace), wbytes,
-        _stream())
-    _check(st, "paged_attention")
+    lib = load()
+    need = 0 if workspace is not None else \
+        lib.paged_attention_workspace_size(b, max_q, max_ctx, hq, hkv, d)
+    ws, wbytes, _keep = _scratch(workspace, need, dev)
+    st = lib.paged_attention(
+        q.data_ptr(), ldq, k_cache.data_ptr(), v_cache.data_ptr(), pages, page,
+        block_table.data_ptr(), block_table.shape[1], cu.data_ptr(), ctx_lens.data_ptr(),
+        out.data_ptr(), ldo, n, b, max_q, max_ctx, hq, hkv, d, d ** -0.5 if scale is None else scale,
+        ws, wbytes, _raw_stream(dev))
+    if st:
+        _check(st, "paged_attention")
     return out
 
 
@@ -656,49 +686,46 @@ def gdn_forward(q, k, v, alpha, beta, cu, state, max_t: int, state_out=None, sca
     gdn_state_commit).  ``max_t``: the most rows a sequence has; ``scale`` D^-0.5 by default.
     Returns out (q's dtype); rows of no sequence are not written.
     """
+    import torch
     if _elsewhere(q, stream):
-        import torch
         with torch.cuda.device(q.device), torch.cuda.stream(stream):
             return gdn_forward(q, k, v, alpha, beta, cu, state, max_t, state_out, scale, out, workspace)
-    import torch
-    dt = q.dtype
-    if dt not in (torch.float16, torch.float32):
+    dt, dev = q.dtype, q.device
+    if dt is not torch.float16 and dt is not torch.float32:
         raise ValueError(f"q must be float16 or float32, got {dt}")
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _require(t, dt, name)
-        if t.dim() != 3 or not _heads_contiguous(t):
-            raise ValueError(f"{name} must be [N, heads, D], heads contiguous")
+    if q.dim() != 3 or v.dim() != 3 or cu.dim() != 1 or state.dim() != 4:
+        raise ValueError("q and v must be [N, heads, D], cu [B + 1], state [B, H, D, D]")
     n, hk, d = q.shape
-    h = v.shape[1]
-    b = cu.shape[0] - 1
-    if k.shape != q.shape or tuple(v.shape) != (n, h, d) or tuple(state.shape) != (b, h, d, d) or \
-            tuple(alpha.shape) != (n, h) or tuple(beta.shape) != (n, h):
-        raise ValueError("gdn_forward: shapes do not match q [N, Hk, D], v [N, H, D], state [B, H, D, D]")
-    _require(cu, torch.int32, "cu")
-    for t, name in ((alpha, "alpha"), (beta, "beta"), (state, "state"), (state_out, "state_out")):
-        if t is not None:
-            _require(t, torch.float32, name)
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-    if state_out is not None and state_out.shape != state.shape:
-        raise ValueError("state_out must have state's shape")
+    h, b = v.shape[1], cu.shape[0] - 1
+    ldq = _rows(q, dt, dev, "q", n, hk, d)
+    ldk = _rows(k, dt, dev, "k", n, hk, d)
+    ldv = _rows(v, dt, dev, "v", n, h, d)
+    _whole(cu, torch.int32, dev, "cu")
+    _whole(alpha, torch.float32, dev, "alpha")
+    _whole(beta, torch.float32, dev, "beta")
+    _whole(state, torch.float32, dev, "state")
+    if alpha.shape != (n, h) or beta.shape != (n, h) or state.shape != (b, h, d, d):
+        raise ValueError("alpha and beta must be [N, H], state [B, H, D, D]")
+    so = None
+    if state_out is not None:
+        _whole(state_out, torch.float32, dev, "state_out")
+        if state_out.shape != state.shape:
+            raise ValueError("state_out must have state's shape")
+        so = state_out.data_ptr()
     if out is None:
-        out = torch.empty((n, h, d), dtype=dt, device=q.device)
-    _require(out, dt, "out")
-    if out.shape[0] != n or out.numel() != n * h * d or not _heads_contiguous(out):
-        raise ValueError(f"out must be [{n}, {h}, {d}] or [{n}, {h * d}], heads contiguous")
-    need = gdn_forward_workspace_size(n, b, max_t, hk, h, d, dt)
-    if workspace is None and need > 0:
-        workspace = new_workspace(need, q.device)
-    _on_device(q.device, k=k, v=v, alpha=alpha, beta=beta, cu=cu, state=state, state_out=state_out,
-               out=out, workspace=workspace)
-    wbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    st = load().gdn_forward(
-        _ptr(q), _ld(q, hk * d), _ptr(k), _ld(k, hk * d), _ptr(v), _ld(v, h * d), _ptr(alpha),
-        _ptr(beta), _ptr(cu), _ptr(state), _ptr(state_out), _ptr(out), _ld(out, h * d), n, b, max_t,
-        hk, h, d, int(dt == torch.float32), ctypes.c_float(d ** -0.5 if scale is None else scale),
-        _ptr(workspace), wbytes, _stream())
-    _check(st, "gdn_forward")
+        out = torch.empty((n, h, d), dtype=dt, device=dev)
+    ldo = _rows(out, dt, dev, "out", n, h, d)
+    lib = load()
+    f32 = dt is torch.float32
+    need = 0 if workspace is not None else \
+        lib.gdn_forward_workspace_size(n, b, max_t, hk, h, d, f32)
+    ws, wbytes, _keep = _scratch(workspace, need, dev)
+    st = lib.gdn_forward(
+        q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, alpha.data_ptr(), beta.data_ptr(),
+        cu.data_ptr(), state.data_ptr(), so, out.data_ptr(), ldo, n, b, max_t, hk, h, d, f32,
+        d ** -0.5 if scale is None else scale, ws, wbytes, _raw_stream(dev))
+    if st:
+        _check(st, "gdn_forward")
     return out
 
 

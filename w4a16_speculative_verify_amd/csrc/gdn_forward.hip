@@ -395,130 +395,253 @@ __global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a, char* __restr
   }
 }
 
-constexpr int kScanWaves = 2;              // dv tiles (16 state rows each) per block
+// The scan: a block walks the chunks of one head for NV tiles of 16 state rows
+// (dv).  Per tile, a state wave holds S^T [D x 16] in its accumulators and
+// computes X = K S^T, E = V - G X, U = T diag(beta) E and S' = G_63 S + (R[63] U)^T K;
+// an output wave computes o = scale G Q S^T + A U beside it.  Both waves of a tile
+// read the state and U as operands: the state wave leaves them in LDS as the
+// fragments it uses itself.  One more wave copies the next chunk's K, Q, V rows
+// and fragments into the other half of a double buffer (LDS DMA), so that
+// nothing waits for memory inside a chunk.  Two barriers a chunk:
+//   1  the chunk's copies have landed, S is in LDS
+//   2  U is in LDS (and the output wave is done with S)
+template <int D, int NV>
+struct Scan {
+  static constexpr int DS = D / 32, MT = D / 16;
+  static constexpr int kThreads = 64 * (2 * NV + 1);
+  static constexpr uint32_t kRowsB = kC * D * 2;             // K or Q rows
+  static constexpr uint32_t kQ = kRowsB, kF = 2 * kRowsB;    // offsets in a buffer
+  static constexpr uint32_t kGate = kF + 2 * kOffA;
+  static constexpr uint32_t kV = kGate + 1024;
+  static constexpr uint32_t kBuf = kV + kC * NV * 32;
+  static constexpr uint32_t kS = 2 * kBuf;                   // [NV][DS][hi, lo] fragments
+  static constexpr uint32_t kU = kS + NV * DS * 2 * kFragBytes;
+  static constexpr uint32_t kBytes = kU + NV * 4 * kFragBytes;
+  static_assert(kBytes <= 160 * 1024, "the scan's buffers exceed a CU's LDS");
+};
 
-template <int D>
-__global__ __launch_bounds__(64 * kScanWaves) void gdn_scan_kernel(GdnArgs a,
-                                                                   const char* __restrict__ ws) {
-  constexpr int DS = D / 32, MT = D / 16, NT = 64 * kScanWaves;
-  __shared__ __attribute__((aligned(16))) _Float16 s_k[kC * D], s_q[kC * D];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+__device__ __forceinline__ u32x4s rows_rsrc(const void* base, int64_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return u32x4s{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu)),
+                (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)bytes), 0x00020000u};
+}
+
+template <int D, int NV>
+__global__ __launch_bounds__(64 * (2 * NV + 1), 1) void gdn_scan_kernel(GdnArgs a,
+                                                                        const char* __restrict__ ws) {
+  using L = Scan<D, NV>;
+  constexpr int DS = L::DS, MT = L::MT;
+  __shared__ __attribute__((aligned(1024))) unsigned char s_buf[L::kBytes];
+  const uint32_t lds = lds_addr(s_buf);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, grp = lane >> 4;
   const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.H / a.Hk);
-  const int dv = (blockIdx.x * kScanWaves + wave) * 16 + col;
   const Seq sq = seq_of(a, b);
   const int slot0 = sq.start / kC + b;
-
-  // state: lane (dv, grp) holds dk 32 s + 8 grp + 0 .. 7 in tiles 2 s, 2 s + 1
-  const int64_t soff = (((int64_t)b * a.H + h) * D + dv) * D + 8 * grp;
-  f32x4 st[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-    st[m] = *reinterpret_cast<const f32x4*>(a.state + soff + 32 * (m >> 1) + 4 * (m & 1));
-
   const int chunks = (sq.T + kC - 1) / kC;
-  for (int c = 0; c < chunks; ++c) {
-    const int n = min(kC, sq.T - c * kC);
-    const int64_t row0 = sq.start + (int64_t)c * kC;
-    const char* w = ws + ((int64_t)(slot0 + c) * a.H + h) * kSlotBytes;
-    __syncthreads();
-    stage_rows<D, NT>(s_k, static_cast<const _Float16*>(a.k) + row0 * a.ldk + hk * D, a.ldk, n);
-    stage_rows<D, NT>(s_q, static_cast<const _Float16*>(a.q) + row0 * a.ldq + hk * D, a.ldq, n);
-    __syncthreads();
-    const float* gate = reinterpret_cast<const float*>(w + kOffGate);
-    const auto frag = [&](uint32_t off, int tt, int s, int lo) {
-      return *reinterpret_cast<const f16x8*>(w + off + (frag_of(tt, s) * 2 + lo) * kFragBytes + lane * 16);
-    };
-    const auto rows = [&](const _Float16* t, int r, int s) {
-      return *reinterpret_cast<const f16x8*>(t + r * D + (((4 * s + grp) ^ swz<D>(r)) * 8));
-    };
+  const int dv0 = blockIdx.x * NV * 16;
 
-    Pair sp[DS];
+  const auto at = [&](uint32_t off) { return *(W4V_LDS f16x8*)(lds + off); };
+  const auto frag = [&](uint32_t base, int i) { return at(base + i * kFragBytes + lane * 16); };
+  // operand rows tau(tt, .) of K or Q, 32 dk of step s
+  const auto rows = [&](uint32_t base, int tt, int s) {
+    const int r = tau(tt, col);
+    return at(base + r * D * 2 + ((4 * s + grp) ^ swz<D>(r)) * 16);
+  };
+
+  if (wave == 2 * NV) {
+    // ---- the copying wave
+    constexpr int CH = D / 8, CV = 2 * NV;
+    const auto copy = [&](int c) {
+      const uint32_t dst = lds + (c & 1) * L::kBuf;
+      const int n = min(kC, sq.T - c * kC);
+      const int64_t row0 = sq.start + (int64_t)c * kC;
+      const auto* k = static_cast<const _Float16*>(a.k) + row0 * a.ldk + hk * D;
+      const auto* q = static_cast<const _Float16*>(a.q) + row0 * a.ldq + hk * D;
+      const auto* v = static_cast<const _Float16*>(a.v) + row0 * a.ldv + h * D + dv0;
+      // rows at or past n lie behind the resource's end and become zeros
+      const u32x4s rk = rows_rsrc(k, ((int64_t)(n - 1) * a.ldk + D) * 2);
+      const u32x4s rq = rows_rsrc(q, ((int64_t)(n - 1) * a.ldq + D) * 2);
+      const u32x4s rv = rows_rsrc(v, ((int64_t)(n - 1) * a.ldv + NV * 16) * 2);
+      const u32x4s rf = rows_rsrc(ws + ((int64_t)(slot0 + c) * a.H + h) * kSlotBytes, kSlotBytes);
 #pragma unroll
-    for (int s = 0; s < DS; ++s) sp[s] = split(st[2 * s], st[2 * s + 1]);
-    f32x4 e[4], o[4];
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-      f32x4 x{0.f, 0.f, 0.f, 0.f}, y{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < DS; ++s) {
-        const f16x8 kf = rows(s_k, tau(tt, col), s), qf = rows(s_q, tau(tt, col), s);
-        x = mfma16x16x32(kf, sp[s].hi, x);
-        x = mfma16x16x32(kf, sp[s].lo, x);
-        y = mfma16x16x32(qf, sp[s].hi, y);
-        y = mfma16x16x32(qf, sp[s].lo, y);
+      for (int u = 0; u < CH; ++u) {
+        const int e = u * 64 + lane, r = e / CH, ch = (e % CH) ^ swz<D>(r);
+        dma16(dst + u * 1024, rk, (uint32_t)(r * (int)a.ldk * 2 + ch * 16));
       }
-      const int t0 = 32 * (tt >> 1) + 8 * grp + 4 * (tt & 1);
-      const f32x4 g = *reinterpret_cast<const f32x4*>(gate + t0);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = t0 + r;
-        const float v = t < n ? (float)static_cast<const _Float16*>(a.v)[(row0 + t) * a.ldv + h * D + dv] : 0.f;
-        e[tt][r] = v - g[r] * x[r];
-        o[tt][r] = a.scale * g[r] * y[r];
+      for (int u = 0; u < kOffA / 1024; ++u) dma16(dst + L::kF + u * 1024, rf, u * 1024 + lane * 16);
+      dma16(dst + L::kGate, rf, kOffGate + lane * 16);
+#pragma unroll
+      for (int u = 0; u < CV; ++u) {
+        const int e = u * 64 + lane;
+        dma16(dst + L::kV + u * 1024, rv, (uint32_t)(e / CV * (int)a.ldv * 2 + e % CV * 16));
       }
+#pragma unroll
+      for (int u = 0; u < CH; ++u) {
+        const int e = u * 64 + lane, r = e / CH, ch = (e % CH) ^ swz<D>(r);
+        dma16(dst + L::kQ + u * 1024, rq, (uint32_t)(r * (int)a.ldq * 2 + ch * 16));
+      }
+#pragma unroll
+      for (int u = 0; u < kOffA / 1024; ++u)
+        dma16(dst + L::kF + kOffA + u * 1024, rf, kOffA + u * 1024 + lane * 16);
+    };
+    if (chunks > 0) copy(0);
+    for (int c = 0; c < chunks; ++c) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      lds_barrier();
+      if (c + 1 < chunks) copy(c + 1);
+      lds_barrier();
     }
-    const Pair ep[2] = {split(e[0], e[1]), split(e[2], e[3])};
-    f32x4 u[4];
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-      u[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s <= tt / 2; ++s) {
-        const f16x8 th = frag(0, tt, s, 0), tl = frag(0, tt, s, 1);
-        u[tt] = mfma16x16x32(th, ep[s].hi, u[tt]);
-        u[tt] = mfma16x16x32(tl, ep[s].hi, u[tt]);
-        u[tt] = mfma16x16x32(th, ep[s].lo, u[tt]);
-      }
-    }
-    Pair up[2] = {split(u[0], u[1]), split(u[2], u[3])};
-#pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-#pragma unroll
-      for (int s = 0; s <= tt / 2; ++s) {
-        const f16x8 ah = frag(kOffA, tt, s, 0), al = frag(kOffA, tt, s, 1);
-        o[tt] = mfma16x16x32(ah, up[s].hi, o[tt]);
-        o[tt] = mfma16x16x32(al, up[s].hi, o[tt]);
-        o[tt] = mfma16x16x32(ah, up[s].lo, o[tt]);
-      }
-      const int t0 = 32 * (tt >> 1) + 8 * grp + 4 * (tt & 1);
-      const f32x4 d = *reinterpret_cast<const f32x4*>(gate + kC + t0);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        u[tt][r] *= d[r];
-        if (t0 + r < n)
-          static_cast<_Float16*>(a.o)[(row0 + t0 + r) * a.ldo + h * D + dv] = (_Float16)o[tt][r];
-      }
-    }
-    const float gc = gate[kC - 1];
-    up[0] = split(u[0], u[1]);
-    up[1] = split(u[2], u[3]);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) st[m][r] *= gc;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        // rows rho of tile m are dk 32 (m / 2) + 8 (rho / 4) + 4 (m & 1) + rho % 4
-        f16x8 kt;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int t = 32 * s + 8 * grp + 4 * hf + (col >> 2);
-          const int ch = 4 * (m >> 1) + (col & 3);
-          const h16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4f16(
-              (W4V_LDS h16x4*)(lds_addr(s_k) + t * D * 2 + ((ch ^ swz<D>(t)) * 16) + 8 * (m & 1)));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) kt[4 * hf + i] = (_Float16)x[i];
-        }
-        st[m] = mfma16x16x32(kt, up[s].hi, st[m]);
-        st[m] = mfma16x16x32(kt, up[s].lo, st[m]);
-      }
-    }
-  }
-  if (a.state_out != nullptr) {
+  } else if (wave < NV) {
+    // ---- a state wave: lane (dv, grp) holds dk 32 s + 8 grp + 0 .. 7 in tiles 2 s, 2 s + 1
+    const int64_t soff = (((int64_t)b * a.H + h) * D + dv0 + wave * 16 + col) * D + 8 * grp;
+    f32x4 st[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
-      *reinterpret_cast<f32x4*>(a.state_out + soff + 32 * (m >> 1) + 4 * (m & 1)) = st[m];
+      st[m] = *reinterpret_cast<const f32x4*>(a.state + soff + 32 * (m >> 1) + 4 * (m & 1));
+    Pair sp[DS];
+    const auto publish = [&]() {
+#pragma unroll
+      for (int s = 0; s < DS; ++s) {
+        sp[s] = split(st[2 * s], st[2 * s + 1]);
+        const uint32_t f = lds + L::kS + (wave * DS + s) * 2 * kFragBytes + lane * 16;
+        *(W4V_LDS f16x8*)f = sp[s].hi;
+        *(W4V_LDS f16x8*)(f + kFragBytes) = sp[s].lo;
+      }
+    };
+    publish();
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t buf = (c & 1) * L::kBuf;
+      lds_barrier();
+      f32x4 e[4], u[4];
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) e[tt] = u[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < DS; ++s)
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+          const f16x8 kf = rows(buf, tt, s);
+          e[tt] = mfma16x16x32(kf, sp[s].hi, e[tt]);
+          u[tt] = mfma16x16x32(kf, sp[s].lo, u[tt]);
+        }
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        const int t0 = 32 * (tt >> 1) + 8 * grp + 4 * (tt & 1);
+        const f32x4 g = *(W4V_LDS f32x4*)(lds + buf + L::kGate + t0 * 4);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float v = (float)*(W4V_LDS _Float16*)(lds + buf + L::kV +
+                                                      ((t0 + r) * NV * 16 + wave * 16 + col) * 2);
+          e[tt][r] = v - g[r] * (e[tt][r] + u[tt][r]);
+          u[tt][r] = 0.f;
+        }
+      }
+      const Pair ep[2] = {split(e[0], e[1]), split(e[2], e[3])};
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+#pragma unroll
+          for (int tt = 2 * s; tt < 4; ++tt) {
+            const f16x8 t = frag(buf + L::kF, frag_of(tt, s) * 2 + (x == 1));
+            u[tt] = mfma16x16x32(t, x == 2 ? ep[s].lo : ep[s].hi, u[tt]);
+          }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const Pair p = split(u[2 * s], u[2 * s + 1]);
+        const uint32_t f = lds + L::kU + (wave * 2 + s) * 2 * kFragBytes + lane * 16;
+        *(W4V_LDS f16x8*)f = p.hi;
+        *(W4V_LDS f16x8*)(f + kFragBytes) = p.lo;
+      }
+      lds_barrier();
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        const int t0 = 32 * (tt >> 1) + 8 * grp + 4 * (tt & 1);
+        const f32x4 d = *(W4V_LDS f32x4*)(lds + buf + L::kGate + (kC + t0) * 4);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) u[tt][r] *= d[r];
+      }
+      const Pair up[2] = {split(u[0], u[1]), split(u[2], u[3])};
+      const float gc = *(W4V_LDS float*)(lds + buf + L::kGate + (kC - 1) * 4);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) st[m][r] *= gc;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          // rows rho of tile m are dk 32 (m / 2) + 8 (rho / 4) + 4 (m & 1) + rho % 4
+          f16x8 kt;
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const int t = 32 * s + 8 * grp + 4 * hf + (col >> 2);
+            const int ch = 4 * (m >> 1) + (col & 3);
+            const h16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4f16(
+                (W4V_LDS h16x4*)(lds + buf + t * D * 2 + ((ch ^ swz<D>(t)) * 16) + 8 * (m & 1)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) kt[4 * hf + i] = (_Float16)x[i];
+          }
+          st[m] = mfma16x16x32(kt, up[s].hi, st[m]);
+          st[m] = mfma16x16x32(kt, up[s].lo, st[m]);
+        }
+      if (c + 1 < chunks) publish();
+    }
+    if (a.state_out != nullptr) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        *reinterpret_cast<f32x4*>(a.state_out + soff + 32 * (m >> 1) + 4 * (m & 1)) = st[m];
+    }
+  } else {
+    // ---- an output wave
+    const int tile = wave - NV;
+    _Float16* out = static_cast<_Float16*>(a.o) + (int64_t)sq.start * a.ldo + h * D + dv0 + tile * 16 + col;
+    for (int c = 0; c < chunks; ++c) {
+      const uint32_t buf = (c & 1) * L::kBuf;
+      const int n = min(kC, sq.T - c * kC);
+      lds_barrier();
+      f32x4 o[4];
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) o[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < DS; ++s) {
+        const f16x8 sh = frag(L::kS, (tile * DS + s) * 2), sl = frag(L::kS, (tile * DS + s) * 2 + 1);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+          const f16x8 qf = rows(buf + L::kQ, tt, s);
+          o[tt] = mfma16x16x32(qf, sh, o[tt]);
+          o[tt] = mfma16x16x32(qf, sl, o[tt]);
+        }
+      }
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        const int t0 = 32 * (tt >> 1) + 8 * grp + 4 * (tt & 1);
+        const f32x4 g = *(W4V_LDS f32x4*)(lds + buf + L::kGate + t0 * 4);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[tt][r] *= a.scale * g[r];
+      }
+      lds_barrier();
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const f16x8 uh = frag(L::kU, (tile * 2 + s) * 2), ul = frag(L::kU, (tile * 2 + s) * 2 + 1);
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+#pragma unroll
+          for (int tt = 2 * s; tt < 4; ++tt) {
+            const f16x8 t = frag(buf + L::kF + kOffA, frag_of(tt, s) * 2 + (x == 1));
+            o[tt] = mfma16x16x32(t, x == 2 ? ul : uh, o[tt]);
+          }
+      }
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        const int t0 = 32 * (tt >> 1) + 8 * grp + 4 * (tt & 1);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (t0 + r < n) out[((int64_t)c * kC + t0 + r) * a.ldo] = (_Float16)o[tt][r];
+      }
+    }
   }
 }
 
@@ -535,8 +658,8 @@ static void launch_gdn(const GdnArgs& a, const GdnPlan& p, void* ws, hipStream_t
   if (p.chunked) {
     hipLaunchKernelGGL(gdn_chunk_kernel<D>, dim3(a.N / kC + a.B, a.H), dim3(256), 0, stream, a,
                        static_cast<char*>(ws));
-    hipLaunchKernelGGL(gdn_scan_kernel<D>, dim3(D / 16 / kScanWaves, a.H, a.B), dim3(64 * kScanWaves),
-                       0, stream, a, static_cast<const char*>(ws));
+    hipLaunchKernelGGL((gdn_scan_kernel<D, 2>), dim3(D / 32, a.H, a.B), dim3(Scan<D, 2>::kThreads), 0,
+                       stream, a, static_cast<const char*>(ws));
   } else if (a.f32) {
     hipLaunchKernelGGL((gdn_recurrent_kernel<D, float>), dim3(D / kRows, a.H, a.B), dim3(kThreads), 0,
                        stream, a);
