@@ -311,7 +311,8 @@ int gdn_state_commit(float* state, const float* k, const float* v, const float* 
  * state    fp32 [B x H x D x D] (S[b, h] is [dv x dk] row-major), 16-byte aligned;
  *          state_out the same, equal to state (in place), disjoint from it, or NULL.
  *          o and state_out overlap no input (o not q, k, v; state aside).
- * Sizes    D 64 or 128 (W4V_ERR_UNSUPPORTED otherwise); B, H <= 65535.
+ * Sizes    D 64 or 128; B, H <= 65535; row strides of q, k, v below 2^23
+ *          (W4V_ERR_UNSUPPORTED otherwise).
  * max_t    the most rows a sequence has: chooses the form (the results stay right
  *          whatever it is).  fp16 inputs with max_t above 64 take the chunked form: 64
  *          positions at a time on the matrix cores, the state in fp32, every operand

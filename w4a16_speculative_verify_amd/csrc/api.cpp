@@ -747,6 +747,9 @@ int gdn_forward(const void* q, int64_t ldq, const void* k, int64_t ldk, const vo
         !aligned(alpha, 4) || !aligned(beta, 4) || ldq % 8 != 0 || ldk % 8 != 0 || ldv % 8 != 0 ||
         ldo % 8 != 0)
       return W4V_ERR_ALIGNMENT;
+    // the chunked form's copies take 32-bit offsets over the 64 rows of a chunk
+    const int64_t far = int64_t(1) << 23;
+    if (ldq >= far || ldk >= far || ldv >= far) return W4V_ERR_UNSUPPORTED;
     const int es = f32 ? 2 : 1;            // fp16 spans per element
     const size_t gb = (size_t)N * H * 4;
     const struct { const void* p; size_t n; } in[] = {

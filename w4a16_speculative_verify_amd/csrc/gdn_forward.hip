@@ -40,10 +40,6 @@ namespace w4v {
 
 namespace {
 
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-typedef __fp16 h16x4 __attribute__((ext_vector_type(4)));
-#define W4V_LDS __attribute__((address_space(3)))
-
 struct Seq {
   int start, T;      // first row and rows
 };
@@ -75,7 +71,7 @@ __global__ __launch_bounds__(kThreads) void gdn_recurrent_kernel(GdnArgs a) {
   constexpr int CPT = D / kTPR, NC = CPT / 4;
   constexpr int kPer = kStage * D / kThreads;          // staged q (and k) values per thread
   __shared__ __attribute__((aligned(16))) float sq[kStage][D], sk[kStage][D];
-  __shared__ float sv[kStage][kRows], sa[kStage], sb[kStage], skq[kStage];
+  __shared__ float sv[kStage][kRows], sa[kStage], sb[kStage];
 
   const int tid = threadIdx.x, row = tid / kTPR, r = tid % kTPR;
   const int h = blockIdx.y, b = blockIdx.z, row0 = blockIdx.x * kRows;
@@ -177,7 +173,7 @@ __global__ __launch_bounds__(kThreads) void gdn_recurrent_kernel(GdnArgs a) {
 
 // ------------------------------------------------------------------ chunked
 constexpr int kC = kGdnChunk;              // 64 tokens
-constexpr int kLd = kC + 1;                // fp32 rows of the 64 x 64 tiles in LDS
+constexpr int kLd = kC + 4;                // fp32 rows of the 64 x 64 tiles in LDS (16-byte aligned)
 
 // Workspace of one (chunk, head): the fragments of T diag(beta) and of
 // scale R (q.k), as pairs of fp16 (x = hi + lo, 22 bits), in the order in which
@@ -209,10 +205,6 @@ __device__ __forceinline__ int swz(int r) {
   return D == 128 ? 4 * (r & 3) + sg : 4 * ((r >> 1) & 1) + sg;
 }
 
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return (uint32_t)(uintptr_t)(W4V_LDS const void*)p;
-}
-
 // Eight fp32 values (two accumulators' lanes) as fp16 pairs x = hi + lo.  The
 // values are fixed in registers first: a product or sum that the compiler
 // rounded to fp16 once for hi and through fp32 for lo would give a lo that
@@ -222,13 +214,14 @@ struct Pair {
 };
 __device__ __forceinline__ Pair split(const f32x4& x, const f32x4& y) {
   Pair p;
+  float minus = -1.f;                      // hidden: lo is one mixed-precision fma per value
+  asm("" : "+v"(minus));
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     float v = e < 4 ? x[e & 3] : y[e & 3];
     asm("" : "+v"(v));
-    const _Float16 h = (_Float16)v;
-    p.hi[e] = h;
-    p.lo[e] = (_Float16)(v - (float)h);
+    p.hi[e] = (_Float16)v;
+    p.lo[e] = (_Float16)__builtin_fmaf((float)p.hi[e], minus, v);
   }
   return p;
 }
@@ -248,29 +241,38 @@ __device__ __forceinline__ void stage_rows(_Float16* dst, const _Float16* src, i
   }
 }
 
-// acc += A B for 16 x 16 fp32 blocks in LDS (row strides kLd), on the fp32 matrix instruction
-__device__ __forceinline__ void mm16(const float* A, const float* B, f32x4& acc) {
+// acc += A B for 16 x 16 fp32 blocks in LDS (row strides lda, ldb), on the fp32 matrix instruction
+__device__ __forceinline__ void mm16(const float* A, int lda, const float* B, int ldb, f32x4& acc) {
   const int col = threadIdx.x & 15, grp = (threadIdx.x & 63) >> 4;
 #pragma unroll
   for (int kk = 0; kk < 4; ++kk)
-    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(A[col * kLd + 4 * kk + grp],
-                                               B[(4 * kk + grp) * kLd + col], acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(A[col * lda + 4 * kk + grp],
+                                               B[(4 * kk + grp) * ldb + col], acc, 0, 0, 0);
 }
-__device__ __forceinline__ void put16(float* C, const f32x4& v, float sign) {
+__device__ __forceinline__ void put16(float* C, int ldc, const f32x4& v, float sign) {
   const int col = threadIdx.x & 15, grp = (threadIdx.x & 63) >> 4;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) C[(4 * grp + r) * kLd + col] = sign * v[r];
+  for (int r = 0; r < 4; ++r) C[(4 * grp + r) * ldc + col] = sign * v[r];
 }
 
+// One (chunk, head) per block: T diag(beta) and scale R (q.k).  K Q^T and K K^T are
+// formed transposed, with rows and columns in tau order, so that a lane's
+// accumulators are the eight consecutive values of a fragment: scale R (q.k) goes
+// from registers to the workspace, L through LDS into the inversion.  K and Q
+// make room for L and T once they have been read: 42 KiB a block, three blocks a
+// CU, which hide the chain of small steps (loads, products, inversion).
 template <int D>
 __global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a, char* __restrict__ ws) {
   constexpr int DS = D / 32;
-  __shared__ __attribute__((aligned(16))) _Float16 s_k[kC * D], s_q[kC * D];
-  __shared__ float s_r[kC * kLd];          // R, then scale R (q.k)
-  __shared__ float s_l[kC * kLd];          // L
-  __shared__ float s_t[kC * kLd];          // T
-  __shared__ float s_m[4][16 * kLd];
-  __shared__ float s_beta[kC];
+  constexpr int kRowsF = kC * D;                       // K and Q as fp16: D floats a row pair
+  constexpr int kTiles = 2 * kC * kLd;                 // L and T
+  __shared__ __attribute__((aligned(16))) float s_buf[kRowsF > kTiles ? kRowsF : kTiles];
+  __shared__ float s_m[4][16 * 17];
+  __shared__ __attribute__((aligned(16))) float s_alpha[kC], s_beta[kC], s_end[kC][9];
+  _Float16* s_k = reinterpret_cast<_Float16*>(s_buf);
+  _Float16* s_q = s_k + kC * D;
+  float* s_l = s_buf;
+  float* s_t = s_buf + kC * kLd;
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, grp = lane >> 4;
@@ -293,50 +295,86 @@ __global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a, char* __restr
   stage_rows<D, 256>(s_k, static_cast<const _Float16*>(a.k) + row0 * a.ldk + hk * D, a.ldk, n);
   stage_rows<D, 256>(s_q, static_cast<const _Float16*>(a.q) + row0 * a.ldq + hk * D, a.ldq, n);
   if (wave == 0) {
+    // lane t: products of gates from the start of t's block of 8 to t, and on from t to the end
+    // of every block before it: s_end[t][k] = prod of alpha over 8 k + 8 .. t
     const float al = lane < n ? a.alpha[(row0 + lane) * a.H + h] : 1.f;
+    s_alpha[lane] = al;
     s_beta[lane] = lane < n ? a.beta[(row0 + lane) * a.H + h] : 0.f;
-    float r = 0.f, g = 1.f;
-    float* gate = reinterpret_cast<float*>(out + kOffGate);
+    float up = al, down = 1.f;             // prod over block start .. t, and t + 1 .. block end
 #pragma unroll
-    for (int t = 0; t < kC; ++t) {
-      const float at = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, al), t));
-      r = t == lane ? 1.f : r * at;        // zero until the column's own token
-      g *= t <= lane ? at : 1.f;
-      s_r[t * kLd + lane] = r;
+    for (int i = 1; i < 8; ++i) {
+      const float x = __shfl_up(al, i, 64), y = __shfl_down(al, i, 64);
+      if (i <= (lane & 7)) up *= x;
+      if (i <= 7 - (lane & 7)) down *= y;
     }
-    gate[lane] = g;
-    gate[kC + lane] = r;
+    float v = up;
+#pragma unroll
+    for (int k = 6; k >= -1; --k) {        // block k + 1 whole: its last lane's product
+      const float whole = __shfl(up, 8 * (k + 1) + 7, 64);
+      const int own = lane >> 3;
+      if (k + 1 < own) v *= whole;
+      if (k >= 0) s_end[lane][k] = k + 1 <= own ? v : 1.f;
+      if (k + 1 > own) down *= whole;
+    }
+    float* gate = reinterpret_cast<float*>(out + kOffGate);
+    gate[lane] = v;                        // G
+    gate[kC + lane] = down;                // R[63][.]
   }
   __syncthreads();
 
-  // L and scale R (q.k): wave w takes the 16 rows 16 w .. of both
+  // wave w: columns t = tau(w, .), rows i over all tau tiles up to the diagonal's 32
   f32x4 kk[4], qk[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) kk[i] = qk[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const auto rows = [&](const _Float16* t, int r, int s) {
-    return *reinterpret_cast<const f16x8*>(t + r * D + (((4 * s + grp) ^ swz<D>(r)) * 8));
+  const auto rows = [&](const _Float16* x, int tt, int s) {
+    const int r = tau(tt, col);
+    return *reinterpret_cast<const f16x8*>(x + r * D + (((4 * s + grp) ^ swz<D>(r)) * 8));
   };
 #pragma unroll
   for (int s = 0; s < DS; ++s) {
-    const f16x8 ak = rows(s_k, 16 * wave + col, s), aq = rows(s_q, 16 * wave + col, s);
+    const f16x8 bk = rows(s_k, wave, s), bq = rows(s_q, wave, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (i > wave) continue;              // above the diagonal
-      const f16x8 bk = rows(s_k, 16 * i + col, s);
-      kk[i] = mfma16x16x32(ak, bk, kk[i]);
-      qk[i] = mfma16x16x32(aq, bk, qk[i]);
+      if (i / 2 > wave / 2) continue;      // tokens behind the wave's 32
+      const f16x8 x = rows(s_k, i, s);
+      kk[i] = mfma16x16x32(x, bk, kk[i]);
+      qk[i] = mfma16x16x32(x, bq, qk[i]);
     }
   }
+  const int t = tau(wave, col);
+  const float bt = s_beta[t];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = 16 * wave + 4 * grp + r, j = 16 * i + col;
-      const float d = s_r[t * kLd + j];
-      s_l[t * kLd + j] = j < t ? s_beta[t] * d * kk[i][r] : 0.f;
-      s_r[t * kLd + j] = j <= t ? a.scale * d * qk[i][r] : 0.f;
-      s_t[t * kLd + j] = 0.f;
+  for (int s = 0; s < 2; ++s) {
+    if (s > wave / 2) {
+      kk[2 * s] = kk[2 * s + 1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      continue;
     }
+    const int i0 = 32 * s + 8 * grp;       // R[t][i0 + 7] .. R[t][i0]
+    float r = i0 + 8 <= t ? s_end[t][i0 / 8] : 1.f;
+#pragma unroll
+    for (int e = 7; e >= 0; --e) {
+      const float d = i0 + e <= t ? r : 0.f;
+      f32x4& x = kk[2 * s + e / 4];
+      f32x4& y = qk[2 * s + e / 4];
+      x[e & 3] = i0 + e < t ? bt * d * x[e & 3] : 0.f;
+      y[e & 3] = i0 + e <= t ? a.scale * d * y[e & 3] : 0.f;
+      if (i0 + e <= t) r *= s_alpha[i0 + e];
+    }
+    const Pair y = split(qk[2 * s], qk[2 * s + 1]);
+    char* f = out + kOffA + (wave < 2 ? wave : 2 * wave - 2 + s) * 2 * kFragBytes + lane * 16;
+    *reinterpret_cast<f16x8*>(f) = y.hi;
+    *reinterpret_cast<f16x8*>(f + kFragBytes) = y.lo;
+  }
+  __syncthreads();                         // K and Q have been read
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    float* l = s_l + t * kLd + 32 * s + 8 * grp;
+    *reinterpret_cast<f32x4*>(l) = kk[2 * s];
+    *reinterpret_cast<f32x4*>(l + 4) = kk[2 * s + 1];
+    float* z = s_t + t * kLd + 32 * s + 8 * grp;
+    *reinterpret_cast<f32x4*>(z) = f32x4{0.f, 0.f, 0.f, 0.f};
+    *reinterpret_cast<f32x4*>(z + 4) = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
   __syncthreads();
 
   // T = (I + L)^-1: the diagonal blocks by forward substitution (lane j: column
@@ -346,52 +384,54 @@ __global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a, char* __restr
   if (lane < 16) {
     float x[16];
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
-      float y = t == lane ? 1.f : 0.f;
+    for (int r = 0; r < 16; ++r) {
+      float y = r == lane ? 1.f : 0.f;
 #pragma unroll
-      for (int i = 0; i < t; ++i) y = __builtin_fmaf(-s_l[(o16 + t) * kLd + o16 + i], x[i], y);
-      x[t] = y;
-      s_t[(o16 + t) * kLd + o16 + lane] = y;
+      for (int i = 0; i < r; i += 4) {
+        const f32x4 l = *reinterpret_cast<const f32x4*>(s_l + (o16 + r) * kLd + o16 + i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e < r) y = __builtin_fmaf(-l[e], x[i + e], y);
+      }
+      x[r] = y;
+      s_t[(o16 + r) * kLd + o16 + lane] = y;
     }
   }
   __syncthreads();
 #pragma unroll
   for (int d = 1; d < 4; ++d) {
     const int i = wave + d, j = wave;      // block (i, j) of this diagonal
-    f32x4 m{0.f, 0.f, 0.f, 0.f};
     if (i < 4) {
+      f32x4 m{0.f, 0.f, 0.f, 0.f};
       for (int k = j; k < i; ++k)
-        mm16(s_l + 16 * i * kLd + 16 * k, s_t + 16 * k * kLd + 16 * j, m);
-      put16(s_m[wave], m, 1.f);
-    }
-    __syncthreads();
-    if (i < 4) {
+        mm16(s_l + 16 * i * kLd + 16 * k, kLd, s_t + 16 * k * kLd + 16 * j, kLd, m);
+      put16(s_m[wave], 17, m, 1.f);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");     // the wave's own scratch
       m = f32x4{0.f, 0.f, 0.f, 0.f};
-      mm16(s_t + 16 * i * kLd + 16 * i, s_m[wave], m);
-      put16(s_t + 16 * i * kLd + 16 * j, m, -1.f);
+      mm16(s_t + 16 * i * kLd + 16 * i, kLd, s_m[wave], 17, m);
+      put16(s_t + 16 * i * kLd + 16 * j, kLd, m, -1.f);
     }
     __syncthreads();
   }
 
-  // fragments: wave w writes those of token tile w
+  // fragments of T diag(beta): wave w writes those of token tile w
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     if (s > wave / 2) continue;
-    const int t = tau(wave, col), i0 = 32 * s + 8 * grp;
-    f32x4 x0, x1, y0, y1;
+    const int i0 = 32 * s + 8 * grp;
+    const float* r = s_t + t * kLd + i0;
+    f32x4 x0 = *reinterpret_cast<const f32x4*>(r), x1 = *reinterpret_cast<const f32x4*>(r + 4);
+    const f32x4 b0 = *reinterpret_cast<const f32x4*>(s_beta + i0);
+    const f32x4 b1 = *reinterpret_cast<const f32x4*>(s_beta + i0 + 4);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      x0[e] = s_t[t * kLd + i0 + e] * s_beta[i0 + e];
-      x1[e] = s_t[t * kLd + i0 + 4 + e] * s_beta[i0 + 4 + e];
-      y0[e] = s_r[t * kLd + i0 + e];
-      y1[e] = s_r[t * kLd + i0 + 4 + e];
+      x0[e] *= b0[e];
+      x1[e] *= b1[e];
     }
-    const Pair x = split(x0, x1), y = split(y0, y1);
+    const Pair x = split(x0, x1);
     char* f = out + (wave < 2 ? wave : 2 * wave - 2 + s) * 2 * kFragBytes + lane * 16;
     *reinterpret_cast<f16x8*>(f) = x.hi;
     *reinterpret_cast<f16x8*>(f + kFragBytes) = x.lo;
-    *reinterpret_cast<f16x8*>(f + kOffA) = y.hi;
-    *reinterpret_cast<f16x8*>(f + kOffA + kFragBytes) = y.lo;
   }
 }
 
@@ -420,13 +460,6 @@ struct Scan {
   static_assert(kBytes <= 160 * 1024, "the scan's buffers exceed a CU's LDS");
 };
 
-__device__ __forceinline__ u32x4s rows_rsrc(const void* base, int64_t bytes) {
-  const uint64_t a = reinterpret_cast<uint64_t>(base);
-  return u32x4s{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
-                (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu)),
-                (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)bytes), 0x00020000u};
-}
-
 template <int D, int NV>
 __global__ __launch_bounds__(64 * (2 * NV + 1), 1) void gdn_scan_kernel(GdnArgs a,
                                                                         const char* __restrict__ ws) {
@@ -442,13 +475,18 @@ __global__ __launch_bounds__(64 * (2 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
   const int chunks = (sq.T + kC - 1) / kC;
   const int dv0 = blockIdx.x * NV * 16;
 
-  const auto at = [&](uint32_t off) { return *(W4V_LDS f16x8*)(lds + off); };
-  const auto frag = [&](uint32_t base, int i) { return at(base + i * kFragBytes + lane * 16); };
-  // operand rows tau(tt, .) of K or Q, 32 dk of step s
-  const auto rows = [&](uint32_t base, int tt, int s) {
-    const int r = tau(tt, col);
-    return at(base + r * D * 2 + ((4 * s + grp) ^ swz<D>(r)) * 16);
-  };
+  const auto at = [&](uint32_t off) { return lds_get<f16x8>(off); };
+  // offsets of a lane's operand reads: rows tau(tt, .), 32 dk of step s (the swizzle is that of
+  // row tau(0, col) for every tt)
+  uint32_t ro[DS];
+#pragma unroll
+  for (int s = 0; s < DS; ++s)
+    ro[s] = lds + tau(0, col) * D * 2 + ((4 * s + grp) ^ swz<D>(tau(0, col))) * 16;
+  constexpr uint32_t kTile[4] = {0, 4 * D * 2, 32 * D * 2, 36 * D * 2};
+  const uint32_t fo = lds + lane * 16;
+  // lane's first token in a tile pair, and its gates
+  const uint32_t go = lds + L::kGate + 8 * grp * 4;
+  constexpr uint32_t kTok[4] = {0, 4, 32, 36};
 
   if (wave == 2 * NV) {
     // ---- the copying wave
@@ -461,10 +499,10 @@ __global__ __launch_bounds__(64 * (2 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
       const auto* q = static_cast<const _Float16*>(a.q) + row0 * a.ldq + hk * D;
       const auto* v = static_cast<const _Float16*>(a.v) + row0 * a.ldv + h * D + dv0;
       // rows at or past n lie behind the resource's end and become zeros
-      const u32x4s rk = rows_rsrc(k, ((int64_t)(n - 1) * a.ldk + D) * 2);
-      const u32x4s rq = rows_rsrc(q, ((int64_t)(n - 1) * a.ldq + D) * 2);
-      const u32x4s rv = rows_rsrc(v, ((int64_t)(n - 1) * a.ldv + NV * 16) * 2);
-      const u32x4s rf = rows_rsrc(ws + ((int64_t)(slot0 + c) * a.H + h) * kSlotBytes, kSlotBytes);
+      const u32x4s rk = dma_rsrc(k, (uint32_t)((n - 1) * (int)a.ldk + D) * 2);
+      const u32x4s rq = dma_rsrc(q, (uint32_t)((n - 1) * (int)a.ldq + D) * 2);
+      const u32x4s rv = dma_rsrc(v, (uint32_t)((n - 1) * (int)a.ldv + NV * 16) * 2);
+      const u32x4s rf = dma_rsrc(ws + ((int64_t)(slot0 + c) * a.H + h) * kSlotBytes, kSlotBytes);
 #pragma unroll
       for (int u = 0; u < CH; ++u) {
         const int e = u * 64 + lane, r = e / CH, ch = (e % CH) ^ swz<D>(r);
@@ -494,21 +532,29 @@ __global__ __launch_bounds__(64 * (2 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
       if (c + 1 < chunks) copy(c + 1);
       lds_barrier();
     }
-  } else if (wave < NV) {
+  } else if (wave >= NV) {
     // ---- a state wave: lane (dv, grp) holds dk 32 s + 8 grp + 0 .. 7 in tiles 2 s, 2 s + 1
-    const int64_t soff = (((int64_t)b * a.H + h) * D + dv0 + wave * 16 + col) * D + 8 * grp;
+    __builtin_amdgcn_s_setprio(2);
+    const int tile = wave - NV;
+    const int64_t soff = (((int64_t)b * a.H + h) * D + dv0 + tile * 16 + col) * D + 8 * grp;
     f32x4 st[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
       st[m] = *reinterpret_cast<const f32x4*>(a.state + soff + 32 * (m >> 1) + 4 * (m & 1));
     Pair sp[DS];
+    const uint32_t so = fo + L::kS + tile * DS * 2 * kFragBytes;
+    const uint32_t uo = fo + L::kU + tile * 4 * kFragBytes;
+    const uint32_t vo = lds + L::kV + (8 * grp * NV * 16 + tile * 16 + col) * 2;
+    const int tr = 8 * grp + (col >> 2);   // the lane's token of a transposing read
+    uint32_t ko[DS];
+#pragma unroll
+    for (int s = 0; s < DS; ++s) ko[s] = lds + tr * D * 2 + ((4 * s + (col & 3)) ^ swz<D>(tr)) * 16;
     const auto publish = [&]() {
 #pragma unroll
       for (int s = 0; s < DS; ++s) {
         sp[s] = split(st[2 * s], st[2 * s + 1]);
-        const uint32_t f = lds + L::kS + (wave * DS + s) * 2 * kFragBytes + lane * 16;
-        *(W4V_LDS f16x8*)f = sp[s].hi;
-        *(W4V_LDS f16x8*)(f + kFragBytes) = sp[s].lo;
+        lds_put(so + s * 2 * kFragBytes, sp[s].hi);
+        lds_put(so + (s * 2 + 1) * kFragBytes, sp[s].lo);
       }
     };
     publish();
@@ -519,21 +565,21 @@ __global__ __launch_bounds__(64 * (2 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) e[tt] = u[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int s = 0; s < DS; ++s)
+      for (int s = 0; s < DS; ++s) {
+        const uint32_t r = ro[s] + buf;
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
-          const f16x8 kf = rows(buf, tt, s);
+          const f16x8 kf = at(r + kTile[tt]);
           e[tt] = mfma16x16x32(kf, sp[s].hi, e[tt]);
           u[tt] = mfma16x16x32(kf, sp[s].lo, u[tt]);
         }
+      }
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
-        const int t0 = 32 * (tt >> 1) + 8 * grp + 4 * (tt & 1);
-        const f32x4 g = *(W4V_LDS f32x4*)(lds + buf + L::kGate + t0 * 4);
+        const f32x4 g = lds_get<f32x4>(go + buf + kTok[tt] * 4);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float v = (float)*(W4V_LDS _Float16*)(lds + buf + L::kV +
-                                                      ((t0 + r) * NV * 16 + wave * 16 + col) * 2);
+          const float v = (float)lds_get<_Float16>(vo + buf + (kTok[tt] + r) * NV * 32);
           e[tt][r] = v - g[r] * (e[tt][r] + u[tt][r]);
           u[tt][r] = 0.f;
         }
@@ -545,26 +591,20 @@ __global__ __launch_bounds__(64 * (2 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
         for (int x = 0; x < 3; ++x)
 #pragma unroll
           for (int tt = 2 * s; tt < 4; ++tt) {
-            const f16x8 t = frag(buf + L::kF, frag_of(tt, s) * 2 + (x == 1));
+            const f16x8 t = at(fo + buf + L::kF + (frag_of(tt, s) * 2 + (x == 1)) * kFragBytes);
             u[tt] = mfma16x16x32(t, x == 2 ? ep[s].lo : ep[s].hi, u[tt]);
           }
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const Pair p = split(u[2 * s], u[2 * s + 1]);
-        const uint32_t f = lds + L::kU + (wave * 2 + s) * 2 * kFragBytes + lane * 16;
-        *(W4V_LDS f16x8*)f = p.hi;
-        *(W4V_LDS f16x8*)(f + kFragBytes) = p.lo;
-      }
+      for (int tt = 0; tt < 4; ++tt) lds_put(uo + tt * kFragBytes, u[tt]);
       lds_barrier();
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
-        const int t0 = 32 * (tt >> 1) + 8 * grp + 4 * (tt & 1);
-        const f32x4 d = *(W4V_LDS f32x4*)(lds + buf + L::kGate + (kC + t0) * 4);
+        const f32x4 d = lds_get<f32x4>(go + buf + (kC + kTok[tt]) * 4);
 #pragma unroll
         for (int r = 0; r < 4; ++r) u[tt][r] *= d[r];
       }
       const Pair up[2] = {split(u[0], u[1]), split(u[2], u[3])};
-      const float gc = *(W4V_LDS float*)(lds + buf + L::kGate + (kC - 1) * 4);
+      const float gc = lds_get<float>(lds + buf + L::kGate + (kC - 1) * 4);
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -574,16 +614,8 @@ __global__ __launch_bounds__(64 * (2 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           // rows rho of tile m are dk 32 (m / 2) + 8 (rho / 4) + 4 (m & 1) + rho % 4
-          f16x8 kt;
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const int t = 32 * s + 8 * grp + 4 * hf + (col >> 2);
-            const int ch = 4 * (m >> 1) + (col & 3);
-            const h16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4f16(
-                (W4V_LDS h16x4*)(lds + buf + t * D * 2 + ((ch ^ swz<D>(t)) * 16) + 8 * (m & 1)));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) kt[4 * hf + i] = (_Float16)x[i];
-          }
+          const uint32_t k = ko[m >> 1] + buf + 32 * s * D * 2 + 8 * (m & 1);
+          const f16x8 kt = join8(lds_get_tr(k), lds_get_tr(k + 4 * D * 2));
           st[m] = mfma16x16x32(kt, up[s].hi, st[m]);
           st[m] = mfma16x16x32(kt, up[s].lo, st[m]);
         }
@@ -596,50 +628,60 @@ __global__ __launch_bounds__(64 * (2 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
     }
   } else {
     // ---- an output wave
-    const int tile = wave - NV;
-    _Float16* out = static_cast<_Float16*>(a.o) + (int64_t)sq.start * a.ldo + h * D + dv0 + tile * 16 + col;
-    for (int c = 0; c < chunks; ++c) {
+    const int tile = wave;
+    const uint32_t so = fo + L::kS + tile * DS * 2 * kFragBytes;
+    const uint32_t uo = fo + L::kU + tile * 4 * kFragBytes;
+    _Float16* out = static_cast<_Float16*>(a.o) + (int64_t)(sq.start + 8 * grp) * a.ldo + h * D + dv0 +
+                    tile * 16 + col;
+    for (int c = 0; c < chunks; ++c, out += kC * a.ldo) {
       const uint32_t buf = (c & 1) * L::kBuf;
-      const int n = min(kC, sq.T - c * kC);
+      const int n = min(kC, sq.T - c * kC) - 8 * grp;
       lds_barrier();
       f32x4 o[4];
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) o[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < DS; ++s) {
-        const f16x8 sh = frag(L::kS, (tile * DS + s) * 2), sl = frag(L::kS, (tile * DS + s) * 2 + 1);
+        const f16x8 sh = at(so + s * 2 * kFragBytes), sl = at(so + (s * 2 + 1) * kFragBytes);
+        const uint32_t r = ro[s] + buf + L::kQ;
+        f16x8 qf[4];
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-          const f16x8 qf = rows(buf + L::kQ, tt, s);
-          o[tt] = mfma16x16x32(qf, sh, o[tt]);
-          o[tt] = mfma16x16x32(qf, sl, o[tt]);
-        }
+        for (int tt = 0; tt < 4; ++tt) qf[tt] = at(r + kTile[tt]);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) o[tt] = mfma16x16x32(qf[tt], sh, o[tt]);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) o[tt] = mfma16x16x32(qf[tt], sl, o[tt]);
       }
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) {
-        const int t0 = 32 * (tt >> 1) + 8 * grp + 4 * (tt & 1);
-        const f32x4 g = *(W4V_LDS f32x4*)(lds + buf + L::kGate + t0 * 4);
+        const f32x4 g = lds_get<f32x4>(go + buf + kTok[tt] * 4);
 #pragma unroll
         for (int r = 0; r < 4; ++r) o[tt][r] *= a.scale * g[r];
       }
       lds_barrier();
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const f16x8 uh = frag(L::kU, (tile * 2 + s) * 2), ul = frag(L::kU, (tile * 2 + s) * 2 + 1);
+        const Pair u = split(lds_get<f32x4>(uo + 2 * s * kFragBytes),
+                             lds_get<f32x4>(uo + (2 * s + 1) * kFragBytes));
 #pragma unroll
         for (int x = 0; x < 3; ++x)
 #pragma unroll
           for (int tt = 2 * s; tt < 4; ++tt) {
-            const f16x8 t = frag(buf + L::kF + kOffA, frag_of(tt, s) * 2 + (x == 1));
-            o[tt] = mfma16x16x32(t, x == 2 ? ul : uh, o[tt]);
+            const f16x8 t = at(fo + buf + L::kF + kOffA + (frag_of(tt, s) * 2 + (x == 1)) * kFragBytes);
+            o[tt] = mfma16x16x32(t, x == 2 ? u.lo : u.hi, o[tt]);
           }
       }
+      if (n >= (int)kTok[3] + 4) {              // all of the lane's tokens
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        const int t0 = 32 * (tt >> 1) + 8 * grp + 4 * (tt & 1);
+        for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (t0 + r < n) out[((int64_t)c * kC + t0 + r) * a.ldo] = (_Float16)o[tt][r];
+          for (int r = 0; r < 4; ++r) out[(int64_t)(kTok[tt] + r) * a.ldo] = (_Float16)o[tt][r];
+      } else {
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if ((int)kTok[tt] + r < n) out[(int64_t)(kTok[tt] + r) * a.ldo] = (_Float16)o[tt][r];
       }
     }
   }

@@ -8,10 +8,6 @@ namespace w4v {
 
 namespace {
 
-typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-typedef __fp16 h16x4 __attribute__((ext_vector_type(4)));
-#define W4V_LDS __attribute__((address_space(3)))
-
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr uint32_t kRing = 128 * 1024;     // LDS: the waves' key/value rings, then the merge
@@ -29,10 +25,6 @@ struct Ring {
   static constexpr int kPer = 2 * NG * kDma;             // and per tile
 };
 
-__device__ __forceinline__ uint32_t lds_addr(const void* p) {
-  return (uint32_t)(uintptr_t)(W4V_LDS const void*)p;
-}
-
 // Chunk (16 bytes) swizzles inside a group's rows, see the layout notes above.
 template <int D>
 __device__ __forceinline__ int swz_k(int r) {
@@ -41,13 +33,6 @@ __device__ __forceinline__ int swz_k(int r) {
 template <int D>
 __device__ __forceinline__ int swz_v(int r) {
   return D == 64 ? ((r >> 1) & 3) * 2 : (2 * r) & 15;
-}
-
-__device__ __forceinline__ u32x4s rsrc_of(const void* base, uint32_t bytes) {
-  const uint64_t a = reinterpret_cast<uint64_t>(base);
-  return u32x4s{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
-                (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu)),
-                (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00020000u};
 }
 
 // the larger (or the sum) of the four lanes that hold one column
@@ -150,7 +135,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
       const int64_t off =
           pg < 0 ? 0 : (((int64_t)pg * a.Hkv + h) * a.page_size + (key & (a.page_size - 1))) * D;
       const uint32_t bytes = pg < 0 ? 0u : (uint32_t)min(16, end - key) * (D * 2);
-      const u32x4s rk = rsrc_of(a.k_cache + off, bytes), rv = rsrc_of(a.v_cache + off, bytes);
+      const u32x4s rk = dma_rsrc(a.k_cache + off, bytes), rv = dma_rsrc(a.v_cache + off, bytes);
       const uint32_t dst = ring + slot * L::kTile + gi * L::kGroup;
 #pragma unroll
       for (int u = 0; u < L::kDma; ++u) {
@@ -205,7 +190,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
       for (int rt = 0; rt < RT; ++rt) sc[rt][gi] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < DS; ++s) {
-        const f16x8 k = *(W4V_LDS f16x8*)(kb + gi * L::kGroup + ka[s]);
+        const f16x8 k = lds_get<f16x8>(kb + gi * L::kGroup + ka[s]);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) sc[rt][gi] = mfma16x16x32(k, q[rt][s], sc[rt][gi]);
       }
@@ -255,22 +240,12 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
     }
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
-      const h16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4f16((W4V_LDS h16x4*)(vb + va[d]));
       if constexpr (NG == 2) {
-        const h16x4 v1 =
-            __builtin_amdgcn_ds_read_tr16_b64_v4f16((W4V_LDS h16x4*)(vb + L::kGroup + va[d]));
-        f16x8 v;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          v[r] = (_Float16)v0[r];
-          v[4 + r] = (_Float16)v1[r];
-        }
+        const f16x8 v = join8(lds_get_tr(vb + va[d]), lds_get_tr(vb + L::kGroup + va[d]));
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) o[rt][d] = mfma16x16x32(v, p[rt], o[rt][d]);
       } else {
-        f16x4 v;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = (_Float16)v0[r];
+        const f16x4 v = lds_get_tr(vb + va[d]);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
           o[rt][d] = __builtin_amdgcn_mfma_f32_16x16x16f16(v, p4[rt], o[rt][d], 0, 0, 0);
