@@ -217,11 +217,15 @@ __device__ __forceinline__ Pair split(const f32x4& x, const f32x4& y) {
   float minus = -1.f;                      // hidden: lo is one mixed-precision fma per value
   asm("" : "+v"(minus));
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float v = e < 4 ? x[e & 3] : y[e & 3];
-    asm("" : "+v"(v));
-    p.hi[e] = (_Float16)v;
-    p.lo[e] = (_Float16)__builtin_fmaf((float)p.hi[e], minus, v);
+  for (int e = 0; e < 8; e += 2) {
+    float v = e < 4 ? x[e & 3] : y[e & 3], w = e < 4 ? x[(e & 3) + 1] : y[(e & 3) + 1];
+    asm("" : "+v"(v), "+v"(w));
+    f16x2 h = {(_Float16)v, (_Float16)w};
+    asm("" : "+v"(h));                     // one conversion serves hi and the remainder
+    p.hi[e] = h[0];
+    p.hi[e + 1] = h[1];
+    p.lo[e] = (_Float16)__builtin_fmaf((float)h[0], minus, v);
+    p.lo[e + 1] = (_Float16)__builtin_fmaf((float)h[1], minus, w);
   }
   return p;
 }
@@ -436,48 +440,59 @@ __global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a, char* __restr
 }
 
 // The scan: a block walks the chunks of one head for NV tiles of 16 state rows
-// (dv).  Per tile, a state wave holds S^T [D x 16] in its accumulators and
-// computes X = K S^T, E = V - G X, U = T diag(beta) E and S' = G_63 S + (R[63] U)^T K;
-// an output wave computes o = scale G Q S^T + A U beside it.  Both waves of a tile
-// read the state and U as operands: the state wave leaves them in LDS as the
-// fragments it uses itself.  One more wave copies the next chunk's K, Q, V rows
-// and fragments into the other half of a double buffer (LDS DMA), so that
-// nothing waits for memory inside a chunk.  Two barriers a chunk:
+// (dv).  Its time is the chain X = K S^T, E = V - G X, U = T diag(beta) E,
+// S' = G_63 S + (R[63] U)^T K of one chunk after the other, and a wave issues its
+// products, conversions and LDS accesses one by one, so the chain of a tile is
+// dealt to two state waves: wave hf holds S^T [D/2 x 16] (its half of dk) in
+// accumulators and takes token tiles 2 hf, 2 hf + 1 of E.  They exchange partial
+// sums of X and U through LDS.  An output wave a tile computes
+// o = scale G Q S^T + A U beside them, from the same fragments, and one more wave
+// copies the next chunk's K, Q, V rows and fragments into the other half of a
+// double buffer (LDS DMA), so that nothing waits for memory inside a chunk.
+// Three barriers a chunk:
 //   1  the chunk's copies have landed, S is in LDS
-//   2  U is in LDS (and the output wave is done with S)
+//   2  the halves' X of the other's tokens are in LDS
+//   3  U is in LDS: that of tokens 0 .. 31, and of 32 .. 63 in two addends (and
+//      the output wave is done with S)
 template <int D, int NV>
 struct Scan {
   static constexpr int DS = D / 32, MT = D / 16;
-  static constexpr int kThreads = 64 * (2 * NV + 1);
+  static constexpr int kThreads = 64 * (3 * NV + 1);
   static constexpr uint32_t kRowsB = kC * D * 2;             // K or Q rows
   static constexpr uint32_t kQ = kRowsB, kF = 2 * kRowsB;    // offsets in a buffer
   static constexpr uint32_t kGate = kF + 2 * kOffA;
   static constexpr uint32_t kV = kGate + 1024;
   static constexpr uint32_t kBuf = kV + kC * NV * 32;
   static constexpr uint32_t kS = 2 * kBuf;                   // [NV][DS][hi, lo] fragments
-  static constexpr uint32_t kU = kS + NV * DS * 2 * kFragBytes;
-  static constexpr uint32_t kBytes = kU + NV * 4 * kFragBytes;
+  static constexpr uint32_t kX = kS + NV * DS * 2 * kFragBytes;   // [NV][pair][2]
+  static constexpr uint32_t kU = kX + NV * 4 * kFragBytes;        // [NV][U0, U1 of half 0, of half 1][2]
+  static constexpr uint32_t kBytes = kU + NV * 6 * kFragBytes;
   static_assert(kBytes <= 160 * 1024, "the scan's buffers exceed a CU's LDS");
 };
 
 template <int D, int NV>
-__global__ __launch_bounds__(64 * (2 * NV + 1), 1) void gdn_scan_kernel(GdnArgs a,
+__global__ __launch_bounds__(64 * (3 * NV + 1), 1) void gdn_scan_kernel(GdnArgs a,
                                                                         const char* __restrict__ ws) {
   using L = Scan<D, NV>;
-  constexpr int DS = L::DS, MT = L::MT;
+  constexpr int DS = L::DS, HS = DS / 2;
   __shared__ __attribute__((aligned(1024))) unsigned char s_buf[L::kBytes];
   const uint32_t lds = lds_addr(s_buf);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, grp = lane >> 4;
-  const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.H / a.Hk);
+  // blocks are dealt over the eight XCDs one by one: the dv tiles of a head share its rows and
+  // fragments in one XCD's L2
+  constexpr int kTiles = D / 16 / NV;
+  const int place = blockIdx.x >> 3, head = (place / kTiles) * 8 + (blockIdx.x & 7);
+  if (head >= a.H * a.B) return;
+  const int h = head % a.H, b = head / a.H, hk = h / (a.H / a.Hk);
   const Seq sq = seq_of(a, b);
   const int slot0 = sq.start / kC + b;
   const int chunks = (sq.T + kC - 1) / kC;
-  const int dv0 = blockIdx.x * NV * 16;
+  const int dv0 = place % kTiles * NV * 16;
 
   const auto at = [&](uint32_t off) { return lds_get<f16x8>(off); };
-  // offsets of a lane's operand reads: rows tau(tt, .), 32 dk of step s (the swizzle is that of
-  // row tau(0, col) for every tt)
+  // offsets of a lane's operand reads: rows tau(tt, .), 32 dk of step s (every tt has the swizzle
+  // of row tau(0, col))
   uint32_t ro[DS];
 #pragma unroll
   for (int s = 0; s < DS; ++s)
@@ -488,201 +503,269 @@ __global__ __launch_bounds__(64 * (2 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
   const uint32_t go = lds + L::kGate + 8 * grp * 4;
   constexpr uint32_t kTok[4] = {0, 4, 32, 36};
 
-  if (wave == 2 * NV) {
+  if (wave == 3 * NV) {
     // ---- the copying wave
     constexpr int CH = D / 8, CV = 2 * NV;
-    const auto copy = [&](int c) {
+    const auto copy = [&](int c, int part) {   // part 0: K and V, T and the gates; part 1: Q, A
       const uint32_t dst = lds + (c & 1) * L::kBuf;
       const int n = min(kC, sq.T - c * kC);
       const int64_t row0 = sq.start + (int64_t)c * kC;
-      const auto* k = static_cast<const _Float16*>(a.k) + row0 * a.ldk + hk * D;
-      const auto* q = static_cast<const _Float16*>(a.q) + row0 * a.ldq + hk * D;
-      const auto* v = static_cast<const _Float16*>(a.v) + row0 * a.ldv + h * D + dv0;
       // rows at or past n lie behind the resource's end and become zeros
-      const u32x4s rk = dma_rsrc(k, (uint32_t)((n - 1) * (int)a.ldk + D) * 2);
-      const u32x4s rq = dma_rsrc(q, (uint32_t)((n - 1) * (int)a.ldq + D) * 2);
-      const u32x4s rv = dma_rsrc(v, (uint32_t)((n - 1) * (int)a.ldv + NV * 16) * 2);
       const u32x4s rf = dma_rsrc(ws + ((int64_t)(slot0 + c) * a.H + h) * kSlotBytes, kSlotBytes);
+      const int64_t ld = part == 0 ? a.ldk : a.ldq;
+      const auto* x = static_cast<const _Float16*>(part == 0 ? a.k : a.q) + row0 * ld + hk * D;
+      const u32x4s rx = dma_rsrc(x, (uint32_t)((n - 1) * (int)ld + D) * 2);
+      const uint32_t to = dst + (part == 0 ? 0u : L::kQ), ff = part * kOffA;
 #pragma unroll
       for (int u = 0; u < CH; ++u) {
         const int e = u * 64 + lane, r = e / CH, ch = (e % CH) ^ swz<D>(r);
-        dma16(dst + u * 1024, rk, (uint32_t)(r * (int)a.ldk * 2 + ch * 16));
-      }
-#pragma unroll
-      for (int u = 0; u < kOffA / 1024; ++u) dma16(dst + L::kF + u * 1024, rf, u * 1024 + lane * 16);
-      dma16(dst + L::kGate, rf, kOffGate + lane * 16);
-#pragma unroll
-      for (int u = 0; u < CV; ++u) {
-        const int e = u * 64 + lane;
-        dma16(dst + L::kV + u * 1024, rv, (uint32_t)(e / CV * (int)a.ldv * 2 + e % CV * 16));
-      }
-#pragma unroll
-      for (int u = 0; u < CH; ++u) {
-        const int e = u * 64 + lane, r = e / CH, ch = (e % CH) ^ swz<D>(r);
-        dma16(dst + L::kQ + u * 1024, rq, (uint32_t)(r * (int)a.ldq * 2 + ch * 16));
+        dma16(to + u * 1024, rx, (uint32_t)(r * (int)ld * 2 + ch * 16));
       }
 #pragma unroll
       for (int u = 0; u < kOffA / 1024; ++u)
-        dma16(dst + L::kF + kOffA + u * 1024, rf, kOffA + u * 1024 + lane * 16);
+        dma16(dst + L::kF + ff + u * 1024, rf, ff + u * 1024 + lane * 16);
+      if (part == 0) {
+        const auto* v = static_cast<const _Float16*>(a.v) + row0 * a.ldv + h * D + dv0;
+        const u32x4s rv = dma_rsrc(v, (uint32_t)((n - 1) * (int)a.ldv + NV * 16) * 2);
+        dma16(dst + L::kGate, rf, kOffGate + lane * 16);
+#pragma unroll
+        for (int u = 0; u < CV; ++u) {
+          const int e = u * 64 + lane;
+          dma16(dst + L::kV + u * 1024, rv, (uint32_t)(e / CV * (int)a.ldv * 2 + e % CV * 16));
+        }
+      }
     };
-    if (chunks > 0) copy(0);
+    if (chunks > 0) {
+      copy(0, 0);
+      copy(0, 1);
+    }
     for (int c = 0; c < chunks; ++c) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       lds_barrier();
-      if (c + 1 < chunks) copy(c + 1);
+      if (c + 1 < chunks) copy(c + 1, 0);
+      lds_barrier();
+      if (c + 1 < chunks) copy(c + 1, 1);
       lds_barrier();
     }
   } else if (wave >= NV) {
-    // ---- a state wave: lane (dv, grp) holds dk 32 s + 8 grp + 0 .. 7 in tiles 2 s, 2 s + 1
-    __builtin_amdgcn_s_setprio(2);
-    const int tile = wave - NV;
-    const int64_t soff = (((int64_t)b * a.H + h) * D + dv0 + tile * 16 + col) * D + 8 * grp;
-    f32x4 st[MT];
+    // ---- a state wave: lane (dv, grp) holds dk 32 s + 8 grp + 0 .. 7 of its half's steps s in
+    // tiles 2 s, 2 s + 1
+    const int tile = (wave - NV) >> 1, hf = (wave - NV) & 1;
+    const int s0 = hf * HS;                // first step of the half
+    const int64_t soff =
+        (((int64_t)b * a.H + h) * D + dv0 + tile * 16 + col) * D + 32 * s0 + 8 * grp;
+    f32x4 st[2 * HS];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < 2 * HS; ++m)
       st[m] = *reinterpret_cast<const f32x4*>(a.state + soff + 32 * (m >> 1) + 4 * (m & 1));
-    Pair sp[DS];
-    const uint32_t so = fo + L::kS + tile * DS * 2 * kFragBytes;
-    const uint32_t uo = fo + L::kU + tile * 4 * kFragBytes;
-    const uint32_t vo = lds + L::kV + (8 * grp * NV * 16 + tile * 16 + col) * 2;
+    Pair sp[HS];
+    const uint32_t so = fo + L::kS + (tile * DS + s0) * 2 * kFragBytes;
+    const uint32_t xo = fo + L::kX + tile * 4 * kFragBytes;
+    const uint32_t uo = fo + L::kU + tile * 6 * kFragBytes;
     const int tr = 8 * grp + (col >> 2);   // the lane's token of a transposing read
-    uint32_t ko[DS];
+    uint32_t ko[HS], rh[HS];
 #pragma unroll
-    for (int s = 0; s < DS; ++s) ko[s] = lds + tr * D * 2 + ((4 * s + (col & 3)) ^ swz<D>(tr)) * 16;
-    const auto publish = [&]() {
-#pragma unroll
-      for (int s = 0; s < DS; ++s) {
-        sp[s] = split(st[2 * s], st[2 * s + 1]);
-        lds_put(so + s * 2 * kFragBytes, sp[s].hi);
-        lds_put(so + (s * 2 + 1) * kFragBytes, sp[s].lo);
-      }
+    for (int s = 0; s < HS; ++s) {
+      ko[s] = lds + tr * D * 2 + ((4 * (s0 + s) + (col & 3)) ^ swz<D>(tr)) * 16;
+      rh[s] = lds + tau(0, col) * D * 2 + ((4 * (s0 + s) + grp) ^ swz<D>(tau(0, col))) * 16;
+    }
+    // of the half's token pair: gates, values, fragments of T diag(beta) ([s = 0] of both pairs
+    // for half 0, [s = 1] of the second for half 1)
+    const uint32_t gh = go + 32 * hf * 4;
+    const uint32_t vh = lds + L::kV + ((8 * grp + 32 * hf) * NV * 16 + tile * 16 + col) * 2;
+    const auto publish = [&](int s) {
+      sp[s] = split(st[2 * s], st[2 * s + 1]);
+      lds_put(so + s * 2 * kFragBytes, sp[s].hi);
+      lds_put(so + (s * 2 + 1) * kFragBytes, sp[s].lo);
     };
-    publish();
+#pragma unroll
+    for (int s = 0; s < HS; ++s) publish(s);
     for (int c = 0; c < chunks; ++c) {
       const uint32_t buf = (c & 1) * L::kBuf;
       lds_barrier();
-      f32x4 e[4], u[4];
+      // ---- X over the half's dk: the other half's tokens first
+      f32x4 x[2][2];
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) e[tt] = u[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int p = 0; p < 2; ++p) {
+        const uint32_t po = buf + (p == 0 ? 1 - hf : hf) * kTile[2];
+        x[p][0] = x[p][1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int s = 0; s < DS; ++s) {
-        const uint32_t r = ro[s] + buf;
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-          const f16x8 kf = at(r + kTile[tt]);
-          e[tt] = mfma16x16x32(kf, sp[s].hi, e[tt]);
-          u[tt] = mfma16x16x32(kf, sp[s].lo, u[tt]);
+        for (int s = 0; s < HS; ++s) {
+          const f16x8 k0 = at(rh[s] + po), k1 = at(rh[s] + po + kTile[1]);
+          x[p][0] = mfma16x16x32(k0, sp[s].hi, x[p][0]);
+          x[p][1] = mfma16x16x32(k1, sp[s].hi, x[p][1]);
+          x[p][0] = mfma16x16x32(k0, sp[s].lo, x[p][0]);
+          x[p][1] = mfma16x16x32(k1, sp[s].lo, x[p][1]);
         }
       }
+      const uint32_t xw = xo + (1 - hf) * 2 * kFragBytes, xr = xo + hf * 2 * kFragBytes;
+      lds_put(xw, x[0][0]);
+      lds_put(xw + kFragBytes, x[0][1]);
+      // what E needs besides
+      f32x4 g[2], d[4], e[2];
+      _Float16 v[2][4];
+      f16x8 th[4], tl[4];                  // half 0: tiles 0 .. 3 at s = 0; half 1: tiles 2, 3 at s = 1
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        const f32x4 g = lds_get<f32x4>(go + buf + kTok[tt] * 4);
+      for (int i = 0; i < 2; ++i) {
+        g[i] = lds_get<f32x4>(gh + buf + kTok[i] * 4);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float v = (float)lds_get<_Float16>(vo + buf + (kTok[tt] + r) * NV * 32);
-          e[tt][r] = v - g[r] * (e[tt][r] + u[tt][r]);
-          u[tt][r] = 0.f;
+        for (int r = 0; r < 4; ++r) v[i][r] = lds_get<_Float16>(vh + buf + (kTok[i] + r) * NV * 32);
+      }
+      if (hf == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          th[i] = at(fo + buf + L::kF + frag_of(i, 0) * 2 * kFragBytes);
+          tl[i] = at(fo + buf + L::kF + (frag_of(i, 0) * 2 + 1) * kFragBytes);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          th[i] = at(fo + buf + L::kF + frag_of(2 + i, 1) * 2 * kFragBytes);
+          tl[i] = at(fo + buf + L::kF + (frag_of(2 + i, 1) * 2 + 1) * kFragBytes);
         }
       }
-      const Pair ep[2] = {split(e[0], e[1]), split(e[2], e[3])};
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int x = 0; x < 3; ++x)
-#pragma unroll
-          for (int tt = 2 * s; tt < 4; ++tt) {
-            const f16x8 t = at(fo + buf + L::kF + (frag_of(tt, s) * 2 + (x == 1)) * kFragBytes);
-            u[tt] = mfma16x16x32(t, x == 2 ? ep[s].lo : ep[s].hi, u[tt]);
-          }
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt) lds_put(uo + tt * kFragBytes, u[tt]);
       lds_barrier();
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        const f32x4 d = lds_get<f32x4>(go + buf + (kC + kTok[tt]) * 4);
+      for (int i = 0; i < 2; ++i) {
+        const f32x4 y = lds_get<f32x4>(xr + i * kFragBytes);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) u[tt][r] *= d[r];
+        for (int r = 0; r < 4; ++r) e[i][r] = (float)v[i][r] - g[i][r] * (x[1][i][r] + y[r]);
       }
-      const Pair up[2] = {split(u[0], u[1]), split(u[2], u[3])};
+      const Pair ep = split(e[0], e[1]);
+      // ---- U: half 0 gives tokens 0 .. 31 and one addend of 32 .. 63, half 1 the other
+      f32x4 u[4];
+      const auto te = [&](int i, f32x4& y) {
+        y = mfma16x16x32(th[i], ep.hi, f32x4{0.f, 0.f, 0.f, 0.f});
+        y = mfma16x16x32(tl[i], ep.hi, y);
+        y = mfma16x16x32(th[i], ep.lo, y);
+      };
+      if (hf == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) te(i, u[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lds_put(uo + i * kFragBytes, u[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) te(i, u[2 + i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) lds_put(uo + (4 + i) * kFragBytes, u[2 + i]);
+      }
+      // ---- S': what does not need U meanwhile
+      f16x8 k[HS][2][2];
+#pragma unroll
+      for (int s = 0; s < HS; ++s)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            // rows rho of tile m are dk 32 (m / 2) + 8 (rho / 4) + 4 (m & 1) + rho % 4
+            const uint32_t o = ko[s] + buf + 32 * p * D * 2 + 8 * m;
+            k[s][p][m] = join8(lds_get_tr(o), lds_get_tr(o + 4 * D * 2));
+          }
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) d[tt] = lds_get<f32x4>(go + buf + (kC + kTok[tt]) * 4);
       const float gc = lds_get<float>(lds + buf + L::kGate + (kC - 1) * 4);
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < 2 * HS; ++m)
 #pragma unroll
         for (int r = 0; r < 4; ++r) st[m][r] *= gc;
+      lds_barrier();
+      if (hf == 0) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+        for (int i = 0; i < 2; ++i) u[2 + i] += lds_get<f32x4>(uo + (4 + i) * kFragBytes);
+      } else {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          // rows rho of tile m are dk 32 (m / 2) + 8 (rho / 4) + 4 (m & 1) + rho % 4
-          const uint32_t k = ko[m >> 1] + buf + 32 * s * D * 2 + 8 * (m & 1);
-          const f16x8 kt = join8(lds_get_tr(k), lds_get_tr(k + 4 * D * 2));
-          st[m] = mfma16x16x32(kt, up[s].hi, st[m]);
-          st[m] = mfma16x16x32(kt, up[s].lo, st[m]);
+        for (int i = 0; i < 2; ++i) {
+          u[i] = lds_get<f32x4>(uo + i * kFragBytes);
+          u[2 + i] = lds_get<f32x4>(uo + (2 + i) * kFragBytes) + u[2 + i];
         }
-      if (c + 1 < chunks) publish();
+      }
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) u[2 * p + i][r] *= d[2 * p + i][r];
+        const Pair up = split(u[2 * p], u[2 * p + 1]);
+#pragma unroll
+        for (int m = 0; m < 2 * HS; ++m) st[m] = mfma16x16x32(k[m >> 1][p][m & 1], up.hi, st[m]);
+#pragma unroll
+        for (int m = 0; m < 2 * HS; ++m) st[m] = mfma16x16x32(k[m >> 1][p][m & 1], up.lo, st[m]);
+      }
+#pragma unroll
+      for (int s = 0; s < HS; ++s) publish(s);
     }
     if (a.state_out != nullptr) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < 2 * HS; ++m)
         *reinterpret_cast<f32x4*>(a.state_out + soff + 32 * (m >> 1) + 4 * (m & 1)) = st[m];
     }
   } else {
-    // ---- an output wave
+    // ---- an output wave: o^T, so that a lane holds four neighbours of one token's row (the
+    // operands' layouts are the same on both sides)
     const int tile = wave;
     const uint32_t so = fo + L::kS + tile * DS * 2 * kFragBytes;
-    const uint32_t uo = fo + L::kU + tile * 4 * kFragBytes;
-    _Float16* out = static_cast<_Float16*>(a.o) + (int64_t)(sq.start + 8 * grp) * a.ldo + h * D + dv0 +
-                    tile * 16 + col;
+    const uint32_t uo = fo + L::kU + tile * 6 * kFragBytes;
+    _Float16* out = static_cast<_Float16*>(a.o) + (int64_t)(sq.start + tau(0, col)) * a.ldo + h * D + dv0 +
+                    tile * 16 + 4 * grp;
     for (int c = 0; c < chunks; ++c, out += kC * a.ldo) {
       const uint32_t buf = (c & 1) * L::kBuf;
-      const int n = min(kC, sq.T - c * kC) - 8 * grp;
+      const int n = min(kC, sq.T - c * kC) - tau(0, col);
       lds_barrier();
-      f32x4 o[4];
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt) o[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+      Pair sp[DS];
 #pragma unroll
       for (int s = 0; s < DS; ++s) {
-        const f16x8 sh = at(so + s * 2 * kFragBytes), sl = at(so + (s * 2 + 1) * kFragBytes);
-        const uint32_t r = ro[s] + buf + L::kQ;
-        f16x8 qf[4];
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) qf[tt] = at(r + kTile[tt]);
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) o[tt] = mfma16x16x32(qf[tt], sh, o[tt]);
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) o[tt] = mfma16x16x32(qf[tt], sl, o[tt]);
+        sp[s].hi = at(so + s * 2 * kFragBytes);
+        sp[s].lo = at(so + (s * 2 + 1) * kFragBytes);
       }
+      f32x4 o[4];
+      const auto qs = [&](int tp) {        // scale G Q S^T of token tiles 2 tp, 2 tp + 1
 #pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        const f32x4 g = lds_get<f32x4>(go + buf + kTok[tt] * 4);
+        for (int tt = 2 * tp; tt < 2 * tp + 2; ++tt) {
+          o[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[tt][r] *= a.scale * g[r];
+          for (int s = 0; s < DS; ++s) {
+            const f16x8 qf = at(ro[s] + buf + L::kQ + kTile[tt]);
+            o[tt] = mfma16x16x32(sp[s].hi, qf, o[tt]);
+            o[tt] = mfma16x16x32(sp[s].lo, qf, o[tt]);
+          }
+          const float g = a.scale * lds_get<float>(lds + buf + L::kGate + (tau(0, col) + kTok[tt]) * 4);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[tt][r] *= g;
+        }
+      };
+      qs(0);
+      lds_barrier();
+      qs(1);
+      f16x8 ah[kFrags], al[kFrags];
+#pragma unroll
+      for (int i = 0; i < kFrags; ++i) {
+        ah[i] = at(fo + buf + L::kF + kOffA + i * 2 * kFragBytes);
+        al[i] = at(fo + buf + L::kF + kOffA + (i * 2 + 1) * kFragBytes);
       }
       lds_barrier();
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const Pair u = split(lds_get<f32x4>(uo + 2 * s * kFragBytes),
-                             lds_get<f32x4>(uo + (2 * s + 1) * kFragBytes));
+        f32x4 u0 = lds_get<f32x4>(uo + 2 * s * kFragBytes);
+        f32x4 u1 = lds_get<f32x4>(uo + (2 * s + 1) * kFragBytes);
+        if (s == 1) {                      // the addends in the state waves' order
+          u0 += lds_get<f32x4>(uo + 4 * kFragBytes);
+          u1 += lds_get<f32x4>(uo + 5 * kFragBytes);
+        }
+        const Pair u = split(u0, u1);
 #pragma unroll
         for (int x = 0; x < 3; ++x)
 #pragma unroll
           for (int tt = 2 * s; tt < 4; ++tt) {
-            const f16x8 t = at(fo + buf + L::kF + kOffA + (frag_of(tt, s) * 2 + (x == 1)) * kFragBytes);
-            o[tt] = mfma16x16x32(t, x == 2 ? u.lo : u.hi, o[tt]);
+            const f16x8 t = x == 1 ? al[frag_of(tt, s)] : ah[frag_of(tt, s)];
+            o[tt] = mfma16x16x32(x == 2 ? u.lo : u.hi, t, o[tt]);
           }
       }
-      if (n >= (int)kTok[3] + 4) {              // all of the lane's tokens
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) out[(int64_t)(kTok[tt] + r) * a.ldo] = (_Float16)o[tt][r];
-      } else {
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if ((int)kTok[tt] + r < n) out[(int64_t)(kTok[tt] + r) * a.ldo] = (_Float16)o[tt][r];
-      }
+      for (int tt = 0; tt < 4; ++tt)
+        if ((int)kTok[tt] < n)
+          *reinterpret_cast<f16x4*>(out + kTok[tt] * a.ldo) = f16x4{
+              (_Float16)o[tt][0], (_Float16)o[tt][1], (_Float16)o[tt][2], (_Float16)o[tt][3]};
     }
   }
 }
@@ -695,13 +778,24 @@ size_t gdn_forward_workspace(const GdnPlan& p, int N, int B, int H) {
 
 GdnPlan plan_gdn(int N, int max_t, int f32) { return GdnPlan{N > 0 && !f32 && max_t > 64}; }
 
+template <int D, int NV>
+static void launch_scan(const GdnArgs& a, const void* ws, hipStream_t stream) {
+  const int heads = (a.H * a.B + 7) / 8 * 8;
+  hipLaunchKernelGGL((gdn_scan_kernel<D, NV>), dim3(heads * (D / 16 / NV)), dim3(Scan<D, NV>::kThreads),
+                     0, stream, a, static_cast<const char*>(ws));
+}
+
 template <int D>
 static void launch_gdn(const GdnArgs& a, const GdnPlan& p, void* ws, hipStream_t stream) {
   if (p.chunked) {
     hipLaunchKernelGGL(gdn_chunk_kernel<D>, dim3(a.N / kC + a.B, a.H), dim3(256), 0, stream, a,
                        static_cast<char*>(ws));
-    hipLaunchKernelGGL((gdn_scan_kernel<D, 2>), dim3(D / 32, a.H, a.B), dim3(Scan<D, 2>::kThreads), 0,
-                       stream, a, static_cast<const char*>(ws));
+    // One dv tile a block while every block then has a CU (its waves a SIMD each), two tiles, which
+    // share the copies, for more.  D = 128, one / two tiles a block: 2,048 tokens x 16, 24, 32 heads
+    // (128, 192, 256 blocks of one tile) 59 / 71, 60 / 74, 69 / 83 us; 1,024 tokens x 64, 128 heads
+    // 70 / 57, 123 / 100 us.
+    if ((int64_t)a.B * a.H * (D / 16) <= 256) launch_scan<D, 1>(a, ws, stream);
+    else launch_scan<D, 2>(a, ws, stream);
   } else if (a.f32) {
     hipLaunchKernelGGL((gdn_recurrent_kernel<D, float>), dim3(D / kRows, a.H, a.B), dim3(kThreads), 0,
                        stream, a);
