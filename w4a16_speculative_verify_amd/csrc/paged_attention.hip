@@ -35,13 +35,25 @@ __device__ __forceinline__ int swz_v(int r) {
   return D == 64 ? ((r >> 1) & 3) * 2 : (2 * r) & 15;
 }
 
-// the larger (or the sum) of the four lanes that hold one column
+// the larger (or the sum) of the two lanes that hold one column of a 32 x 32 tile
 template <typename F>
-__device__ __forceinline__ float over_groups(float v, F f) {
+__device__ __forceinline__ float over_halves(float v, F f) {
   const uint32_t u = __builtin_bit_cast(uint32_t, v);
   const auto a = __builtin_amdgcn_permlane32_swap(u, u, false, false);
   const uint32_t a0 = a[0], a1 = a[1];
-  v = f(__builtin_bit_cast(float, a0), __builtin_bit_cast(float, a1));
+  return f(__builtin_bit_cast(float, a0), __builtin_bit_cast(float, a1));
+}
+__device__ __forceinline__ float max_halves(float v) {
+  return over_halves(v, [](float x, float y) { return fmaxf(x, y); });
+}
+__device__ __forceinline__ float sum_halves(float v) {
+  return over_halves(v, [](float x, float y) { return x + y; });
+}
+
+// the larger (or the sum) of the four lanes that hold one column of a 16 x 16 tile
+template <typename F>
+__device__ __forceinline__ float over_groups(float v, F f) {
+  v = over_halves(v, f);
   const uint32_t w = __builtin_bit_cast(uint32_t, v);
   const auto b = __builtin_amdgcn_permlane16_swap(w, w, false, false);
   const uint32_t b0 = b[0], b1 = b[1];
@@ -320,6 +332,219 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
   }
 }
 
+// ------------------------------------------------------------------ many rows
+// keys per tile and tiles in the ring; a wave copies KT / kTileWaves keys of each
+constexpr int kTileWaves = 8;
+constexpr int kTileRows = 32 * kTileWaves;
+template <int D>
+struct TileRing {
+  static constexpr int KT = D == 256 ? 32 : 64;
+  static constexpr int NSub = KT / 32;                   // 32-key steps of a tile
+  static constexpr int NG = KT / 16;                     // 16-key groups (pages end on them)
+  static constexpr int NS = 3;
+  static constexpr uint32_t kHalf = KT * D * 2;          // bytes of a tile's keys (or values)
+  static constexpr int KW = KT / kTileWaves;
+  static constexpr int kDma = KW * D * 2 / 1024;         // DMA instructions per wave and half
+};
+template <int D>
+__device__ __forceinline__ int tswz_k(int r) {
+  return D == 64 ? (r >> 1) & 7 : r & 15;
+}
+template <int D>
+__device__ __forceinline__ int tswz_v(int r) {
+  return D == 64 ? 4 * ((r >> 1) & 1) : 4 * (r & 3);
+}
+
+__device__ __forceinline__ f32x16 mfma32x32x16(const f16x8& a, const f16x8& b, const f32x16& c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+template <int D>
+__global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs a, int splits,
+                                                                       float* __restrict__ part) {
+  using L = TileRing<D>;
+  constexpr int DT = D / 32, DS = D / 16, NSub = L::NSub;
+  __shared__ __attribute__((aligned(1024))) unsigned char s_ring[L::NS * 2 * L::kHalf];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 31, half = lane >> 5;
+  const int G = a.Hq / a.Hkv;
+  const int h = blockIdx.x % a.Hkv, split = blockIdx.x / a.Hkv;
+  const int tile = gridDim.y - 1 - blockIdx.y, b = blockIdx.z;
+  const Seq sq = seq_of(a, b);
+  const int row0 = tile * kTileRows, nrows = sq.T * G;
+  if (row0 >= nrows) return;
+  const int last = min(row0 + kTileRows, nrows) - 1;
+  const int end = max(min(sq.len, sq.p0 + last / G + 1), 0);   // keys any row of the block sees
+  const int nt = (end + L::KT - 1) / L::KT;
+  const int t_lo = (int)((int64_t)nt * split / splits);
+  const int t_hi = (int)((int64_t)nt * (split + 1) / splits);
+
+  // the wave's rows: keys up to all_see every row sees, behind any_see none
+  const int wr0 = row0 + 32 * wave;
+  const int x = min(wr0 + col, nrows - 1), xi = x / G, xg = x % G;
+  const int lim = min(sq.p0 + xi, sq.len - 1);
+  const int all_see = sq.p0 + min(wr0, nrows - 1) / G;
+  const int any_see = wr0 < nrows ? sq.p0 + min(wr0 + 31, nrows - 1) / G : -1;
+
+  f16x8 q[DS];
+  {
+    const _Float16* p = a.q + (int64_t)(sq.start + xi) * a.ldq + (h * G + xg) * D + 8 * half;
+#pragma unroll
+    for (int s = 0; s < DS; ++s) q[s] = *reinterpret_cast<const f16x8*>(p + 16 * s);
+  }
+
+  uint32_t ko[L::kDma], vo[L::kDma];       // source offsets of the lane's chunks
+#pragma unroll
+  for (int u = 0; u < L::kDma; ++u) {
+    const int at = u * 64 + lane, r = at / (D / 8), c = at % (D / 8);
+    ko[u] = (uint32_t)(r * D * 2 + (c ^ tswz_k<D>(wave * L::KW + r)) * 16);
+    vo[u] = (uint32_t)(r * D * 2 + (c ^ tswz_v<D>(wave * L::KW + r)) * 16);
+  }
+  const uint32_t ring = lds_addr(s_ring);
+  const int32_t* table = a.table + (int64_t)b * a.max_pages;
+
+  const auto page_of = [&](int key) -> int {
+    if (key >= end) return -1;
+    const int p = table[key >> a.page_shift];
+    return (unsigned)p < (unsigned)a.num_pages ? p : -1;
+  };
+  const auto issue = [&](int t, int slot) {
+    const int key = t * L::KT + wave * L::KW;
+    const int pg = t < t_hi ? page_of(key) : -1;
+    const int64_t off =
+        pg < 0 ? 0 : (((int64_t)pg * a.Hkv + h) * a.page_size + (key & (a.page_size - 1))) * D;
+    const uint32_t bytes = pg < 0 ? 0u : (uint32_t)min(L::KW, end - key) * (D * 2);
+    const u32x4s rk = dma_rsrc(a.k_cache + off, bytes), rv = dma_rsrc(a.v_cache + off, bytes);
+    const uint32_t dst = ring + slot * 2 * L::kHalf + wave * (L::KW * D * 2);
+#pragma unroll
+    for (int u = 0; u < L::kDma; ++u) {
+      dma16(dst + u * 1024, rk, ko[u]);
+      dma16(dst + L::kHalf + u * 1024, rv, vo[u]);
+    }
+  };
+
+  f32x16 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[d][r] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  const float c = a.scale * 1.44269504088896341f;
+
+  // lane offsets of the operand reads: keys col of a 32-key step, chunks 2 s + half; values for the
+  // transposing reads, keys 4 half + i / 4 of a 16-key step, 16 d of half a row tile
+  const uint32_t kb = ring + col * D * 2;
+  const int kx = tswz_k<D>(col);
+  const int i16 = lane & 15, vkey = 4 * half + (i16 >> 2);
+  const uint32_t vb = ring + L::kHalf + vkey * D * 2 + (i16 & 1) * 8;
+  const int vx = tswz_v<D>(vkey), vc = 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
+
+#pragma unroll
+  for (int s = 0; s + 1 < L::NS; ++s) issue(t_lo + s, s);
+  int slot = 0;
+  for (int t = t_lo; t < t_hi; ++t) {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((L::NS - 2) * 2 * L::kDma) : "memory");
+    lds_barrier();
+    issue(t + L::NS - 1, slot == 0 ? L::NS - 1 : slot - 1);
+    const uint32_t so = slot * 2 * L::kHalf;
+    slot = slot + 1 == L::NS ? 0 : slot + 1;
+    const int key0 = t * L::KT;
+    if (key0 > any_see) continue;          // none of the wave's rows sees the tile
+
+    f32x16 sc[NSub];
+#pragma unroll
+    for (int j = 0; j < NSub; ++j) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) sc[j][r] = 0.f;
+#pragma unroll
+      for (int s = 0; s < DS; ++s) {
+        const f16x8 k = lds_get<f16x8>(kb + so + j * 32 * D * 2 + (((2 * s + half) ^ kx) * 16));
+        sc[j] = mfma32x32x16(k, q[s], sc[j]);
+      }
+    }
+    bool hide = key0 + L::KT - 1 > all_see;
+    uint32_t ok = 0;
+#pragma unroll
+    for (int g = 0; g < L::NG; ++g) ok |= (uint32_t)(page_of(key0 + 16 * g) >= 0) << g;
+    if (hide || ok != (1u << L::NG) - 1) {
+#pragma unroll
+      for (int j = 0; j < NSub; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int kk = 32 * j + 8 * (r / 4) + 4 * half + r % 4;
+          const bool see = key0 + kk <= lim && ((ok >> (2 * j + r / 8)) & 1);
+          sc[j][r] = see ? sc[j][r] : -INFINITY;
+        }
+    }
+    float mx = sc[0][0];
+#pragma unroll
+    for (int j = 0; j < NSub; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) mx = fmaxf(mx, sc[j][r]);
+    mx = max_halves(mx) * c;
+    if (__any(mx > m + kLazy)) {
+      const float mn = fmaxf(m, mx);
+      const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[d][r] *= f;
+    }
+    const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int j = 0; j < NSub; ++j) {
+      f16x8 p[2];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j][r], c, -mu));
+        l += e;
+        p[r / 8][r % 8] = (_Float16)e;
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const uint32_t v = vb + so + (32 * j + 16 * s) * D * 2 + (((4 * d + vc) ^ vx) * 16);
+          o[d] = mfma32x32x16(join8(lds_get_tr(v), lds_get_tr(v + 8 * D * 2)), p[s], o[d]);
+        }
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+
+  l = sum_halves(l);
+  if (wr0 + col >= nrows) return;
+  if (splits == 1) {
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    _Float16* out = a.out + (int64_t)(sq.start + xi) * a.ldo + (h * G + xg) * D + 4 * half;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        f16x4 y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = (_Float16)(o[d][4 * g + e] * inv);
+        *reinterpret_cast<f16x4*>(out + 32 * d + 8 * g) = y;
+      }
+  } else {
+    const int64_t item = (((int64_t)b * a.Hkv + h) * gridDim.y + tile) * splits + split;
+    float* po = part + item * kTileRows * (D + 2);
+    const int r = 32 * wave + col;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<f32x4*>(po + (int64_t)r * D + 32 * d + 8 * g + 4 * half) =
+            f32x4{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
+    if (half == 0) {
+      po[(int64_t)kTileRows * D + 2 * r] = m;
+      po[(int64_t)kTileRows * D + 2 * r + 1] = l;
+    }
+  }
+}
+
 // Joins the splits of one (token, query head) per wave.
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int splits, int row_tiles, int R,
@@ -372,7 +597,17 @@ void launch_stream(const AttnArgs& a, const AttnPlan& p, float* partials, hipStr
 }
 
 template <int D>
+void launch_tile(const AttnArgs& a, const AttnPlan& p, float* partials, hipStream_t stream) {
+  hipLaunchKernelGGL(attn_tile_kernel<D>, dim3(a.Hkv * p.splits, p.row_tiles, a.B),
+                     dim3(64 * kTileWaves), 0, stream, a, p.splits, partials);
+  if (p.splits > 1)
+    hipLaunchKernelGGL(attn_join_kernel<D>, dim3((a.max_q * a.Hq + 3) / 4, a.B), dim3(256), 0,
+                       stream, a, p.splits, p.row_tiles, p.rows, partials);
+}
+
+template <int D>
 void launch_d(const AttnArgs& a, const AttnPlan& p, float* partials, hipStream_t stream) {
+  if (p.rows == kTileRows) return launch_tile<D>(a, p, partials, stream);
   if (p.rows == 16) launch_stream<D, 1>(a, p, partials, stream);
   else if (p.rows == 32) launch_stream<D, 2>(a, p, partials, stream);
   else if constexpr (D != 256) launch_stream<D, 4>(a, p, partials, stream);
@@ -383,7 +618,7 @@ void launch_d(const AttnArgs& a, const AttnPlan& p, float* partials, hipStream_t
 AttnPlan plan_attention(int B, int max_q, int max_ctx, int Hq, int Hkv, int D) {
   AttnPlan p;
   const int64_t rows = (int64_t)max_q * (Hq / Hkv);
-  p.rows = rows <= 16 ? 16 : (rows <= 32 || D == 256 ? 32 : 64);
+  p.rows = rows > 128 ? kTileRows : rows <= 16 ? 16 : (rows <= 32 || D == 256 ? 32 : 64);
   p.row_tiles = (int)((rows + p.rows - 1) / p.rows);
   const int64_t items = (int64_t)B * Hkv * p.row_tiles;
   const int tiles = (max_ctx + 31) / 32;
