@@ -409,9 +409,17 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs 
     const int p = table[key >> a.page_shift];
     return (unsigned)p < (unsigned)a.num_pages ? p : -1;
   };
+  // lane j: the page of the wave's keys in tile pages_at + j, so that the table is read once in 64
+  // tiles and a tile's page costs no wait
+  int pages = -1, pages_at = t_lo - 64;
   const auto issue = [&](int t, int slot) {
+    if (t - pages_at >= 64) {
+      pages_at = t;
+      const int tt = t + lane;
+      pages = tt < t_hi ? page_of(tt * L::KT + wave * L::KW) : -1;
+    }
     const int key = t * L::KT + wave * L::KW;
-    const int pg = t < t_hi ? page_of(key) : -1;
+    const int pg = __builtin_amdgcn_readlane(pages, t - pages_at);
     const int64_t off =
         pg < 0 ? 0 : (((int64_t)pg * a.Hkv + h) * a.page_size + (key & (a.page_size - 1))) * D;
     const uint32_t bytes = pg < 0 ? 0u : (uint32_t)min(L::KW, end - key) * (D * 2);
@@ -423,6 +431,13 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs 
       dma16(dst + L::kHalf + u * 1024, rv, vo[u]);
     }
   };
+  // whether any page of the block's keys lies outside the cache: only then tiles that every row
+  // sees are looked at key by key
+  bool bad = false;
+  for (int k = t_lo * L::KT + 16 * (int)threadIdx.x; k < min(t_hi * L::KT, end);
+       k += 16 * 64 * kTileWaves)
+    bad |= page_of(k) < 0;
+  bad = __syncthreads_or(bad);
 
   f32x16 o[DT];
 #pragma unroll
@@ -463,11 +478,13 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs 
         sc[j] = mfma32x32x16(k, q[s], sc[j]);
       }
     }
-    bool hide = key0 + L::KT - 1 > all_see;
-    uint32_t ok = 0;
+    if (bad || key0 + L::KT - 1 > all_see) {
+      uint32_t ok = (1u << L::NG) - 1;
+      if (bad) {
+        ok = 0;
 #pragma unroll
-    for (int g = 0; g < L::NG; ++g) ok |= (uint32_t)(page_of(key0 + 16 * g) >= 0) << g;
-    if (hide || ok != (1u << L::NG) - 1) {
+        for (int g = 0; g < L::NG; ++g) ok |= (uint32_t)(page_of(key0 + 16 * g) >= 0) << g;
+      }
 #pragma unroll
       for (int j = 0; j < NSub; ++j)
 #pragma unroll
