@@ -333,18 +333,21 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
 }
 
 // ------------------------------------------------------------------ many rows
-// keys per tile and tiles in the ring; a wave copies KT / kTileWaves keys of each
-constexpr int kTileWaves = 8;
-constexpr int kTileRows = 32 * kTileWaves;
-template <int D>
+// NW waves of 32 packed rows, keys per tile and tiles in the ring; a wave copies KT / NW keys of a
+// tile, at most 16, which lie in one page
+template <int D, int NW>
 struct TileRing {
-  static constexpr int KT = D == 256 ? 32 : 64;
+  static constexpr int kRows = 32 * NW;
+  static constexpr int KT = D == 256 || NW == 2 ? 32 : 64;
   static constexpr int NSub = KT / 32;                   // 32-key steps of a tile
   static constexpr int NG = KT / 16;                     // 16-key groups (pages end on them)
-  static constexpr int NS = 3;
   static constexpr uint32_t kHalf = KT * D * 2;          // bytes of a tile's keys (or values)
-  static constexpr int KW = KT / kTileWaves;
+  static constexpr int NS = 2 * kHalf == 32768 ? 2 : 2 * kHalf == 16384 ? 4 : 6;
+  static constexpr int KW = KT / NW;
   static constexpr int kDma = KW * D * 2 / 1024;         // DMA instructions per wave and half
+  // blocks of a CU (registers: D = 256 takes a SIMD's 512 for one wave)
+  static constexpr int kPerCU = NW == 8 ? (D == 64 ? 2 : 1) : 2;
+  static constexpr int kPerSimd = D == 256 ? 1 : NW == 8 ? 2 * kPerCU : 2;
 };
 template <int D>
 __device__ __forceinline__ int tswz_k(int r) {
@@ -359,11 +362,11 @@ __device__ __forceinline__ f32x16 mfma32x32x16(const f16x8& a, const f16x8& b, c
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-template <int D>
-__global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs a, int splits,
-                                                                       float* __restrict__ part) {
-  using L = TileRing<D>;
-  constexpr int DT = D / 32, DS = D / 16, NSub = L::NSub;
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_tile_kernel(
+    AttnArgs a, int splits, float* __restrict__ part) {
+  using L = TileRing<D, NW>;
+  constexpr int DT = D / 32, DS = D / 16, NSub = L::NSub, kTileRows = L::kRows;
   __shared__ __attribute__((aligned(1024))) unsigned char s_ring[L::NS * 2 * L::kHalf];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -435,7 +438,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs 
   // sees are looked at key by key
   bool bad = false;
   for (int k = t_lo * L::KT + 16 * (int)threadIdx.x; k < min(t_hi * L::KT, end);
-       k += 16 * 64 * kTileWaves)
+       k += 16 * 64 * NW)
     bad |= page_of(k) < 0;
   bad = __syncthreads_or(bad);
 
@@ -449,16 +452,20 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs 
 
   // lane offsets of the operand reads: keys col of a 32-key step, chunks 2 s + half; values for the
   // transposing reads, keys 4 half + i / 4 of a 16-key step, 16 d of half a row tile
-  const uint32_t kb = ring + col * D * 2;
-  const int kx = tswz_k<D>(col);
+  uint32_t ka[DS], va[DT];
+#pragma unroll
+  for (int s = 0; s < DS; ++s) ka[s] = ring + col * D * 2 + ((2 * s + half) ^ tswz_k<D>(col)) * 16;
   const int i16 = lane & 15, vkey = 4 * half + (i16 >> 2);
-  const uint32_t vb = ring + L::kHalf + vkey * D * 2 + (i16 & 1) * 8;
-  const int vx = tswz_v<D>(vkey), vc = 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+    va[d] = ring + L::kHalf + vkey * D * 2 + (i16 & 1) * 8 +
+            ((4 * d + 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1)) ^ tswz_v<D>(vkey)) * 16;
 
 #pragma unroll
   for (int s = 0; s + 1 < L::NS; ++s) issue(t_lo + s, s);
   int slot = 0;
   for (int t = t_lo; t < t_hi; ++t) {
+    // tile t has landed, and every wave is done with tile t - 1, whose place the next copy takes
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"((L::NS - 2) * 2 * L::kDma) : "memory");
     lds_barrier();
     issue(t + L::NS - 1, slot == 0 ? L::NS - 1 : slot - 1);
@@ -474,7 +481,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs 
       for (int r = 0; r < 16; ++r) sc[j][r] = 0.f;
 #pragma unroll
       for (int s = 0; s < DS; ++s) {
-        const f16x8 k = lds_get<f16x8>(kb + so + j * 32 * D * 2 + (((2 * s + half) ^ kx) * 16));
+        const f16x8 k = lds_get<f16x8>(ka[s] + so + j * 32 * D * 2);
         sc[j] = mfma32x32x16(k, q[s], sc[j]);
       }
     }
@@ -515,16 +522,19 @@ __global__ __launch_bounds__(64 * kTileWaves, 2) void attn_tile_kernel(AttnArgs 
     for (int j = 0; j < NSub; ++j) {
       f16x8 p[2];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j][r], c, -mu));
-        l += e;
-        p[r / 8][r % 8] = (_Float16)e;
+      for (int r = 0; r < 16; r += 2) {
+        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j][r], c, -mu));
+        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j][r + 1], c, -mu));
+        const f16x2 e = {(_Float16)e0, (_Float16)e1};
+        l = __builtin_amdgcn_fdot2(e, f16x2{(_Float16)1.f, (_Float16)1.f}, l, false);
+        p[r / 8][r % 8] = e[0];
+        p[r / 8][r % 8 + 1] = e[1];
       }
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          const uint32_t v = vb + so + (32 * j + 16 * s) * D * 2 + (((4 * d + vc) ^ vx) * 16);
+          const uint32_t v = va[d] + so + (32 * j + 16 * s) * D * 2;
           o[d] = mfma32x32x16(join8(lds_get_tr(v), lds_get_tr(v + 8 * D * 2)), p[s], o[d]);
         }
     }
@@ -608,26 +618,24 @@ template <int D, int RT>
 void launch_stream(const AttnArgs& a, const AttnPlan& p, float* partials, hipStream_t stream) {
   hipLaunchKernelGGL((attn_stream_kernel<D, RT>), dim3(a.Hkv * p.splits, p.row_tiles, a.B),
                      dim3(kThreads), 0, stream, a, p.splits, partials);
-  if (p.splits > 1)
-    hipLaunchKernelGGL(attn_join_kernel<D>, dim3((a.max_q * a.Hq + 3) / 4, a.B), dim3(256), 0,
-                       stream, a, p.splits, p.row_tiles, p.rows, partials);
 }
 
-template <int D>
+template <int D, int NW>
 void launch_tile(const AttnArgs& a, const AttnPlan& p, float* partials, hipStream_t stream) {
-  hipLaunchKernelGGL(attn_tile_kernel<D>, dim3(a.Hkv * p.splits, p.row_tiles, a.B),
-                     dim3(64 * kTileWaves), 0, stream, a, p.splits, partials);
-  if (p.splits > 1)
-    hipLaunchKernelGGL(attn_join_kernel<D>, dim3((a.max_q * a.Hq + 3) / 4, a.B), dim3(256), 0,
-                       stream, a, p.splits, p.row_tiles, p.rows, partials);
+  hipLaunchKernelGGL((attn_tile_kernel<D, NW>), dim3(a.Hkv * p.splits, p.row_tiles, a.B),
+                     dim3(64 * NW), 0, stream, a, p.splits, partials);
 }
 
 template <int D>
 void launch_d(const AttnArgs& a, const AttnPlan& p, float* partials, hipStream_t stream) {
-  if (p.rows == kTileRows) return launch_tile<D>(a, p, partials, stream);
   if (p.rows == 16) launch_stream<D, 1>(a, p, partials, stream);
   else if (p.rows == 32) launch_stream<D, 2>(a, p, partials, stream);
-  else if constexpr (D != 256) launch_stream<D, 4>(a, p, partials, stream);
+  else if (p.rows == 64) launch_tile<D, 2>(a, p, partials, stream);
+  else if (p.rows == 128) launch_tile<D, 4>(a, p, partials, stream);
+  else if constexpr (D != 256) launch_tile<D, 8>(a, p, partials, stream);
+  if (p.splits > 1)
+    hipLaunchKernelGGL(attn_join_kernel<D>, dim3((a.max_q * a.Hq + 3) / 4, a.B), dim3(256), 0,
+                       stream, a, p.splits, p.row_tiles, p.rows, partials);
 }
 
 }  // namespace
@@ -635,12 +643,16 @@ void launch_d(const AttnArgs& a, const AttnPlan& p, float* partials, hipStream_t
 AttnPlan plan_attention(int B, int max_q, int max_ctx, int Hq, int Hkv, int D) {
   AttnPlan p;
   const int64_t rows = (int64_t)max_q * (Hq / Hkv);
-  p.rows = rows > 128 ? kTileRows : rows <= 16 ? 16 : (rows <= 32 || D == 256 ? 32 : 64);
+  const int most = D == 256 ? 128 : 256;
+  p.rows = 16;
+  while (p.rows < most && p.rows < rows) p.rows *= 2;
   p.row_tiles = (int)((rows + p.rows - 1) / p.rows);
   const int64_t items = (int64_t)B * Hkv * p.row_tiles;
   const int tiles = (max_ctx + 31) / 32;
+  const int blocks = p.rows <= 32 || (p.rows == 256 && D == 128) ? 256 : 512;   // that the CUs hold
   p.splits = 1;
-  if (items < 256) p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({64, 256 / items, tiles / 8}));
+  if (items < blocks)
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({64, blocks / items, tiles / 8}));
   p.partial_bytes = p.splits == 1 ? 0 : (size_t)items * p.splits * p.rows * (D + 2) * sizeof(float);
   return p;
 }
