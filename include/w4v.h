@@ -319,8 +319,9 @@ int gdn_state_commit(float* state, const float* k, const float* v, const float* 
  *          that is not fp16 already as an exact pair of fp16 (22 bits); entries of the
  *          state, or of beta (v - S k), at or past 65,504 overflow there.  Otherwise
  *          positions are taken one by one in fp32.
- * workspace  gdn_forward_workspace_size(...) bytes of scratch (0 for the recurrent
- *          form), 256-byte aligned, no contents expected or kept.
+ * workspace  gdn_forward_workspace_size(...) bytes (0 for the recurrent form),
+ *          256-byte aligned; the first 64 KiB, where other calls keep counters, are
+ *          left alone.
  * ---------------------------------------------------------------------- */
 size_t gdn_forward_workspace_size(int N, int B, int max_t, int Hk, int H, int D, int f32);
 
@@ -389,9 +390,10 @@ int rope_kv_append(const void* qkv, int64_t ldqkv, void* q_out, int64_t ldq,
  *            as they were); max_ctx: the most tokens a sequence has, used for the
  *            launch plan alone.  The plan, and so the order of sums, depends on
  *            B, max_q, max_ctx, Hq, Hkv and D.
- * workspace  paged_attention_workspace_size(...) bytes of scratch (0 for plans
- *            that do not split the context; NULL then), 256-byte aligned, no
- *            contents expected or kept. */
+ * workspace  paged_attention_workspace_size(...) bytes (0 for plans that do not
+ *            split the context; NULL then), 256-byte aligned, zeroed once: arrival
+ *            counters in the first 64 KiB (every call leaves them at zero), then
+ *            fp32 partial results, added in the splits' order. */
 size_t paged_attention_workspace_size(int B, int max_q, int max_ctx, int Hq, int Hkv, int D);
 
 int paged_attention(const void* q, int64_t ldq, const void* k_cache, const void* v_cache,

@@ -542,10 +542,8 @@ def _scratch(workspace, need, device):
     if workspace is None:
         if need == 0:
             return None, 0, None
-        import torch
-        workspace = torch.empty(need + 256, dtype=torch.uint8, device=device)
-        off = -workspace.data_ptr() % 256
-        return workspace.data_ptr() + off, need, workspace
+        workspace = new_workspace(need, device)
+        return workspace.data_ptr(), need, workspace
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace

@@ -661,7 +661,7 @@ size_t paged_attention_workspace_size(int B, int max_q, int max_ctx, int Hq, int
   if (B <= 0 || max_q <= 0 || max_ctx < 0 ||
       paged_sizes(1, B, Hq, Hkv, D, 1, 16, 1) != W4V_OK)
     return 0;
-  return w4v::plan_attention(B, max_q, max_ctx, Hq, Hkv, D).partial_bytes;
+  return w4v::plan_attention(B, max_q, max_ctx, Hq, Hkv, D).workspace;
 }
 
 int paged_attention(const void* q, int64_t ldq, const void* k_cache, const void* v_cache,
@@ -688,7 +688,7 @@ int paged_attention(const void* q, int64_t ldq, const void* k_cache, const void*
     return W4V_ERR_INVALID_ARG;
   const w4v::AttnPlan p = w4v::plan_attention(B, max_q, max_ctx, Hq, Hkv, D);
   if (p.row_tiles > kMaxGridYZ) return W4V_ERR_UNSUPPORTED;
-  st = workspace_check(p.partial_bytes, workspace, workspace_bytes);
+  st = workspace_check(p.workspace, workspace, workspace_bytes);
   if (st != W4V_OK) return st;
   w4v::AttnArgs a;
   a.q = static_cast<const _Float16*>(q);
@@ -705,7 +705,7 @@ int paged_attention(const void* q, int64_t ldq, const void* k_cache, const void*
   a.N = N; a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.D = D;
   a.num_pages = num_pages; a.page_size = page_size; a.page_shift = shift;
   a.max_q = max_q;
-  const hipError_t e = w4v::launch_attention(a, p, static_cast<float*>(workspace),
+  const hipError_t e = w4v::launch_attention(a, p, workspace,
                                              static_cast<hipStream_t>(stream));
   return e == hipSuccess ? W4V_OK : W4V_ERR_HIP;
 }

@@ -71,7 +71,7 @@ __global__ __launch_bounds__(kThreads) void gdn_recurrent_kernel(GdnArgs a) {
   constexpr int CPT = D / kTPR, NC = CPT / 4;
   constexpr int kPer = kStage * D / kThreads;          // staged q (and k) values per thread
   __shared__ __attribute__((aligned(16))) float sq[kStage][D], sk[kStage][D];
-  __shared__ float sv[kStage][kRows], sa[kStage], sb[kStage];
+  __shared__ float sv[kStage][kRows], sa[kStage], sb[kStage], skq[kStage];
 
   const int tid = threadIdx.x, row = tid / kTPR, r = tid % kTPR;
   const int h = blockIdx.y, b = blockIdx.z, row0 = blockIdx.x * kRows;
@@ -132,7 +132,23 @@ __global__ __launch_bounds__(kThreads) void gdn_recurrent_kernel(GdnArgs a) {
       sb[tid] = rb;
     }
     __syncthreads();
+    {
+      // k_t . q_t, 16 threads a token
+      const int t = tid / 16, c = tid % 16;
+      float kq = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(&sk[t][4 * (j * 16 + c)]);
+        const f32x4 y = *reinterpret_cast<const f32x4*>(&sq[t][4 * (j * 16 + c)]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) kq = __builtin_fmaf(x[e], y[e], kq);
+      }
+      kq = sum8(kq);
+      kq += __shfl_xor(kq, 8, 64);
+      if (c == 0) skq[t] = kq;
+    }
     if (t0 + kStage < sq_.T) fetch(t0 + kStage);
+    __syncthreads();
     const int n = min(kStage, sq_.T - t0);
     for (int t = 0; t < n; ++t) {
       float kv[CPT], qv[CPT];
@@ -146,21 +162,19 @@ __global__ __launch_bounds__(kThreads) void gdn_recurrent_kernel(GdnArgs a) {
           qv[4 * j + e] = y[e];
         }
       }
-      float u = 0.f, w = 0.f, kq = 0.f;
+      float u = 0.f, w = 0.f;
 #pragma unroll
       for (int j = 0; j < CPT; ++j) {
         u = __builtin_fmaf(s[j], kv[j], u);
         w = __builtin_fmaf(s[j], qv[j], w);
-        kq = __builtin_fmaf(kv[j], qv[j], kq);
       }
       u = sum8(u);
       w = sum8(w);
-      kq = sum8(kq);
       const float at = sa[t];
       const float cf = sb[t] * (sv[t][row] - at * u);
 #pragma unroll
       for (int j = 0; j < CPT; ++j) s[j] = __builtin_fmaf(at, s[j], cf * kv[j]);
-      if (r == 0) o[(int64_t)(t0 + t) * a.ldo + row] = (X)(a.scale * __builtin_fmaf(at, w, cf * kq));
+      if (r == 0) o[(int64_t)(t0 + t) * a.ldo + row] = (X)(a.scale * __builtin_fmaf(at, w, cf * skq[t]));
     }
   }
   if (a.state_out != nullptr) {
@@ -773,7 +787,7 @@ __global__ __launch_bounds__(64 * (3 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
 }  // namespace
 
 size_t gdn_forward_workspace(const GdnPlan& p, int N, int B, int H) {
-  return p.chunked ? ((size_t)(N / kC) + B) * H * kSlotBytes : 0;
+  return p.chunked ? kTicketRegion + ((size_t)(N / kC) + B) * H * kSlotBytes : 0;
 }
 
 GdnPlan plan_gdn(int N, int max_t, int f32) { return GdnPlan{N > 0 && !f32 && max_t > 64}; }
@@ -788,6 +802,7 @@ static void launch_scan(const GdnArgs& a, const void* ws, hipStream_t stream) {
 template <int D>
 static void launch_gdn(const GdnArgs& a, const GdnPlan& p, void* ws, hipStream_t stream) {
   if (p.chunked) {
+    ws = static_cast<char*>(ws) + kTicketRegion;       // other calls' counters stay zero
     hipLaunchKernelGGL(gdn_chunk_kernel<D>, dim3(a.N / kC + a.B, a.H), dim3(256), 0, stream, a,
                        static_cast<char*>(ws));
     // One dv tile a block while every block then has a CU (its waves a SIMD each), two tiles, which

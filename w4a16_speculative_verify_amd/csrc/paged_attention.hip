@@ -87,6 +87,7 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
 
 template <int D, int RT>
 __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, int splits,
+                                                                  unsigned* __restrict__ tickets,
                                                                   float* __restrict__ part) {
   using L = Ring<D>;
   constexpr int R = 16 * RT, DT = D / 16, DS = D / 32, NG = L::NG;
@@ -281,6 +282,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
   __syncthreads();
 
   // ---- the waves' sums are joined through LDS
+  const int64_t item = ((int64_t)b * a.Hkv + h) * gridDim.y + tile;
   float* so = reinterpret_cast<float*>(s_ring);      // [wave][row][D], chunks of 4 swizzled by row
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
@@ -321,14 +323,53 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
       *reinterpret_cast<f16x4*>(a.out + (int64_t)(sq.start + x / G) * a.ldo + (h * G + x % G) * D +
                                 4 * ch) = y;
     } else {
-      const int64_t item = (((int64_t)b * a.Hkv + h) * gridDim.y + tile) * splits + split;
-      float* po = part + item * R * (D + 2);
-      *reinterpret_cast<f32x4*>(po + (int64_t)r * D + 4 * ch) = acc;
-      if (ch == 0) {
-        po[(int64_t)R * D + 2 * r] = mx;
-        po[(int64_t)R * D + 2 * r + 1] = sum;
+      const rsrc_t po = make_rsrc(part + (item * splits + split) * R * (D + 2));
+      st_agent_x4(po, (uint32_t)(r * D + 4 * ch) * 4, __builtin_bit_cast(u32x4, acc));
+      if (ch == 0)
+        st_agent_x2(po, (uint32_t)(R * D + 2 * r) * 4,
+                    u32x2{__builtin_bit_cast(uint32_t, mx), __builtin_bit_cast(uint32_t, sum)});
+    }
+  }
+  if (splits == 1 || tickets == nullptr) return;
+  // ---- the block that arrives last joins the splits, in their order
+  if (!arrive_last(tickets + item * kTicketStride, splits)) return;
+  const rsrc_t po = make_rsrc(part + item * splits * R * (D + 2));
+  const uint32_t step = (uint32_t)(R * (D + 2)) * 4;
+  for (int i = tid; i < R * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), ch = i % (D / 4), x = row0 + r;
+    if (x >= nrows) break;
+    // running maximum: one pass, the loads of eight splits in flight
+    float mx = -INFINITY, sum = 0.f;
+    f32x4 acc{0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < splits; s0 += 8) {
+      f32x4 v[8];
+      u32x2 ml[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t at = (uint32_t)min(s0 + k, splits - 1) * step;
+        v[k] = __builtin_bit_cast(f32x4, ld_agent_x4(po, at + (uint32_t)(r * D + 4 * ch) * 4));
+        ml[k] = __builtin_amdgcn_raw_buffer_load_b64(po, at + (uint32_t)(R * D + 2 * r) * 4, 0, kSC1);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t mk = ml[k][0], lk = ml[k][1];
+        const float m1 = s0 + k < splits ? __builtin_bit_cast(float, mk) : -INFINITY;
+        const float l1 = __builtin_bit_cast(float, lk);
+        const float mn = fmaxf(mx, m1), mu = mn == -INFINITY ? 0.f : mn;
+        const float f = __builtin_amdgcn_exp2f(mx - mu);
+        const float g = __builtin_amdgcn_exp2f(m1 - mu);
+        sum = sum * f + (m1 == -INFINITY ? 0.f : g * l1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = acc[e] * f + (m1 == -INFINITY ? 0.f : g * v[k][e]);
+        mx = mn;
       }
     }
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    f16x4 y;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = (_Float16)(acc[e] * inv);
+    *reinterpret_cast<f16x4*>(a.out + (int64_t)(sq.start + x / G) * a.ldo + (h * G + x % G) * D +
+                              4 * ch) = y;
   }
 }
 
@@ -390,13 +431,6 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
   const int all_see = sq.p0 + min(wr0, nrows - 1) / G;
   const int any_see = wr0 < nrows ? sq.p0 + min(wr0 + 31, nrows - 1) / G : -1;
 
-  f16x8 q[DS];
-  {
-    const _Float16* p = a.q + (int64_t)(sq.start + xi) * a.ldq + (h * G + xg) * D + 8 * half;
-#pragma unroll
-    for (int s = 0; s < DS; ++s) q[s] = *reinterpret_cast<const f16x8*>(p + 16 * s);
-  }
-
   uint32_t ko[L::kDma], vo[L::kDma];       // source offsets of the lane's chunks
 #pragma unroll
   for (int u = 0; u < L::kDma; ++u) {
@@ -434,6 +468,16 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
       dma16(dst + L::kHalf + u * 1024, rv, vo[u]);
     }
   };
+#pragma unroll
+  for (int s = 0; s + 1 < L::NS; ++s) issue(t_lo + s, s);
+
+  f16x8 q[DS];
+  {
+    const _Float16* p = a.q + (int64_t)(sq.start + xi) * a.ldq + (h * G + xg) * D + 8 * half;
+#pragma unroll
+    for (int s = 0; s < DS; ++s) q[s] = *reinterpret_cast<const f16x8*>(p + 16 * s);
+  }
+
   // whether any page of the block's keys lies outside the cache: only then tiles that every row
   // sees are looked at key by key
   bool bad = false;
@@ -461,8 +505,6 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
     va[d] = ring + L::kHalf + vkey * D * 2 + (i16 & 1) * 8 +
             ((4 * d + 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1)) ^ tswz_v<D>(vkey)) * 16;
 
-#pragma unroll
-  for (int s = 0; s + 1 < L::NS; ++s) issue(t_lo + s, s);
   int slot = 0;
   for (int t = t_lo; t < t_hi; ++t) {
     // tile t has landed, and every wave is done with tile t - 1, whose place the next copy takes
@@ -572,11 +614,13 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
   }
 }
 
-// Joins the splits of one (token, query head) per wave.
+// Joins the splits of one (token, query head) per wave: 64 / (D / 4) splits a load, the loads of
+// eight rounds in flight before the weights are known.  (32 splits of 512 rows of 128: one split a
+// load, eight in flight, took 11 us.)
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int splits, int row_tiles, int R,
                                                         const float* __restrict__ part) {
-  constexpr int PL = D / 64;
+  constexpr int LR = D / 4, SP = 64 / LR;      // lanes a row, splits a load
   const int lane = threadIdx.x & 63;
   const int y = blockIdx.x * 4 + (threadIdx.x >> 6), b = blockIdx.y;
   const Seq sq = seq_of(a, b);
@@ -588,36 +632,54 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int splits, 
   const int64_t step = (int64_t)R * (D + 2);
   float ms = -INFINITY, ls = 0.f;
   if (lane < splits) {
-    ms = base[lane * step + R * D + 2 * r];
-    ls = base[lane * step + R * D + 2 * r + 1];
+    const f32x2 ml = *reinterpret_cast<const f32x2*>(base + lane * step + R * D + 2 * r);
+    ms = ml[0];
+    ls = ml[1];
   }
-  float mx = ms;
+  const float* p = base + (int64_t)r * D + 4 * (lane % LR);
+  f32x4 acc{0.f, 0.f, 0.f, 0.f};
+  float f = 0.f, sum = 0.f;
+  for (int s0 = 0; s0 < splits; s0 += 8 * SP) {
+    f32x4 v[8];
 #pragma unroll
-  for (int k = 1; k < 64; k <<= 1) mx = fmaxf(mx, __shfl_xor(mx, k, 64));
-  const float f = ms == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms - mx);
-  float sum = f * ls;
+    for (int k = 0; k < 8; ++k)
+      v[k] = *reinterpret_cast<const f32x4*>(p + min(s0 + k * SP + lane / LR, splits - 1) * step);
+    if (s0 == 0) {
+      float mx = ms;
 #pragma unroll
-  for (int k = 1; k < 64; k <<= 1) sum += __shfl_xor(sum, k, 64);
-  float acc[PL];
+      for (int k = 1; k < 64; k <<= 1) mx = fmaxf(mx, __shfl_xor(mx, k, 64));
+      f = ms == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms - mx);
+      sum = f * ls;
 #pragma unroll
-  for (int e = 0; e < PL; ++e) acc[e] = 0.f;
-#pragma unroll 8
-  for (int s = 0; s < splits; ++s) {
-    const float w = __shfl(f, s, 64);
-    const float* p = base + s * step + (int64_t)r * D + lane * PL;
+      for (int k = 1; k < 64; k <<= 1) sum += __shfl_xor(sum, k, 64);
+    }
 #pragma unroll
-    for (int e = 0; e < PL; ++e) acc[e] = __builtin_fmaf(w, p[e], acc[e]);
+    for (int k = 0; k < 8; ++k) {
+      const int s = s0 + k * SP + lane / LR;
+      const float w = __shfl(f, s & 63, 64);
+      if (s < splits) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(w, v[k][e], acc[e]);
+      }
+    }
   }
+#pragma unroll
+  for (int k = LR; k < 64; k <<= 1)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor(acc[e], k, 64);
+  if (lane >= LR) return;
   const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-  _Float16* out = a.out + (int64_t)(sq.start + i) * a.ldo + (int64_t)head * D + lane * PL;
+  f16x4 o;
 #pragma unroll
-  for (int e = 0; e < PL; ++e) out[e] = (_Float16)(acc[e] * inv);
+  for (int e = 0; e < 4; ++e) o[e] = (_Float16)(acc[e] * inv);
+  *reinterpret_cast<f16x4*>(a.out + (int64_t)(sq.start + i) * a.ldo + (int64_t)head * D + 4 * lane) = o;
 }
 
 template <int D, int RT>
-void launch_stream(const AttnArgs& a, const AttnPlan& p, float* partials, hipStream_t stream) {
+void launch_stream(const AttnArgs& a, const AttnPlan& p, unsigned* tickets, float* partials,
+                   hipStream_t stream) {
   hipLaunchKernelGGL((attn_stream_kernel<D, RT>), dim3(a.Hkv * p.splits, p.row_tiles, a.B),
-                     dim3(kThreads), 0, stream, a, p.splits, partials);
+                     dim3(kThreads), 0, stream, a, p.splits, tickets, partials);
 }
 
 template <int D, int NW>
@@ -627,13 +689,15 @@ void launch_tile(const AttnArgs& a, const AttnPlan& p, float* partials, hipStrea
 }
 
 template <int D>
-void launch_d(const AttnArgs& a, const AttnPlan& p, float* partials, hipStream_t stream) {
-  if (p.rows == 16) launch_stream<D, 1>(a, p, partials, stream);
-  else if (p.rows == 32) launch_stream<D, 2>(a, p, partials, stream);
+void launch_d(const AttnArgs& a, const AttnPlan& p, void* ws, hipStream_t stream) {
+  unsigned* tickets = p.last_joins ? static_cast<unsigned*>(ws) : nullptr;
+  float* partials = reinterpret_cast<float*>(static_cast<char*>(ws) + kTicketRegion);
+  if (p.rows == 16) launch_stream<D, 1>(a, p, tickets, partials, stream);
+  else if (p.rows == 32) launch_stream<D, 2>(a, p, tickets, partials, stream);
   else if (p.rows == 64) launch_tile<D, 2>(a, p, partials, stream);
   else if (p.rows == 128) launch_tile<D, 4>(a, p, partials, stream);
   else if constexpr (D != 256) launch_tile<D, 8>(a, p, partials, stream);
-  if (p.splits > 1)
+  if (p.splits > 1 && !p.last_joins)
     hipLaunchKernelGGL(attn_join_kernel<D>, dim3((a.max_q * a.Hq + 3) / 4, a.B), dim3(256), 0,
                        stream, a, p.splits, p.row_tiles, p.rows, partials);
 }
@@ -653,11 +717,12 @@ AttnPlan plan_attention(int B, int max_q, int max_ctx, int Hq, int Hkv, int D) {
   p.splits = 1;
   if (items < blocks)
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({64, blocks / items, tiles / 8}));
-  p.partial_bytes = p.splits == 1 ? 0 : (size_t)items * p.splits * p.rows * (D + 2) * sizeof(float);
+  p.last_joins = p.rows <= 32 && std::min<int64_t>(rows, p.rows) * p.splits <= 128;
+  p.workspace = p.splits == 1 ? 0 : kTicketRegion + (size_t)items * p.splits * p.rows * (D + 2) * sizeof(float);
   return p;
 }
 
-hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, float* partials,
+hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* partials,
                             hipStream_t stream) {
   if (a.D == 64) launch_d<64>(a, p, partials, stream);
   else if (a.D == 128) launch_d<128>(a, p, partials, stream);

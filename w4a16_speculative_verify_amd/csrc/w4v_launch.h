@@ -260,10 +260,11 @@ struct AttnPlan {
   int rows;            // packed rows a block takes
   int row_tiles;       // blocks along the packed rows of the longest sequence
   int splits;          // blocks along the context (1 = none)
-  size_t partial_bytes;
+  bool last_joins;     // the last block of a row tile joins its splits (else a second kernel)
+  size_t workspace;    // bytes: counters, then fp32 partials (0 when splits == 1)
 };
 AttnPlan plan_attention(int B, int max_q, int max_ctx, int Hq, int Hkv, int D);
-hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, float* partials,
+hipError_t launch_attention(const AttnArgs& a, const AttnPlan& p, void* workspace,
                             hipStream_t stream);
 
 // ---------------------------------------------------------------- verify
