@@ -314,11 +314,12 @@ int gdn_state_commit(float* state, const float* k, const float* v, const float* 
  * Sizes    D 64 or 128; B, H <= 65535; row strides of q, k, v below 2^23
  *          (W4V_ERR_UNSUPPORTED otherwise).
  * max_t    the most rows a sequence has: chooses the form (the results stay right
- *          whatever it is).  fp16 inputs with max_t above 64 take the chunked form: 64
- *          positions at a time on the matrix cores, the state in fp32, every operand
- *          that is not fp16 already as an exact pair of fp16 (22 bits); entries of the
- *          state, or of beta (v - S k), at or past 65,504 overflow there.  Otherwise
- *          positions are taken one by one in fp32.
+ *          whatever it is).  fp16 inputs with max_t above 16 go 32 positions at a
+ *          time through the matrix cores, above 64 64 at a time, with the state in
+ *          fp32 and every operand that is not fp16 already as a pair of fp16 (22
+ *          bits): entries of the state, or of beta (v - S k), at or past 65,504
+ *          overflow there, and an input that is not finite reaches the outputs of
+ *          all positions it is taken with.  Otherwise positions go one by one in fp32.
  * workspace  gdn_forward_workspace_size(...) bytes (0 for the recurrent form),
  *          256-byte aligned; the first 64 KiB, where other calls keep counters, are
  *          left alone.

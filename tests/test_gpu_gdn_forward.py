@@ -89,7 +89,9 @@ def run(lib, x, max_t=None, steps=32, scale=None, what="", in_place=False, updat
     ([1, 1, 1], 2, 6, 64, np.float16),
     ([16, 3, 0, 17], 4, 4, 128, np.float16),                  # a verify block, a sequence without rows
     ([33, 15, 32], 1, 3, 64, np.float32),
-    ([64], 2, 4, 128, np.float16),                            # the longest recurrent fp16 block
+    ([17, 31, 32, 1, 0], 2, 4, 128, np.float16),              # 32 at a time
+    ([33, 64, 5], 1, 2, 64, np.float16),                      # two rounds of 32
+    ([64], 2, 4, 128, np.float16),                            # the longest block of one kernel
     ([65], 2, 4, 128, np.float16),                            # the shortest chunked one
     ([128, 127, 129, 1, 0, 63], 2, 2, 64, np.float16),
     ([200, 64, 70], 1, 4, 128, np.float16),
@@ -103,7 +105,7 @@ def test_forward_matches_oracle(lib, new, hk, h, d, dtype):
     log(f"  {new} {hk}/{h} d={d}: {w:.2f} of the tolerance")
 
 
-@pytest.mark.parametrize("max_t", [1, 64, 65, 100000])
+@pytest.mark.parametrize("max_t", [1, 16, 17, 64, 65, 100000])
 def test_the_hint_shapes_the_launch_only(lib, max_t):
     """Any max_t gives the result, in either form; sequences in place."""
     rng = np.random.default_rng(max_t)
@@ -133,7 +135,7 @@ def test_no_rows_at_all(lib, dtype):
     torch.cuda.synchronize()
 
 
-@pytest.mark.parametrize("new", [[40], [180]])
+@pytest.mark.parametrize("new", [[14], [40], [180]])
 @pytest.mark.parametrize("case", ["reset", "keep", "repeat", "long_memory", "closed", "negative"])
 def test_gates_at_their_ends(lib, new, case):
     """Decay gates of zero (the state starts anew) and one, full writes of one key over and over
@@ -142,7 +144,7 @@ def test_gates_at_their_ends(lib, new, case):
     q, k, v, al, be, cu, s = inputs(rng, new, 2, 2, 128, np.float16)
     steps = 32
     if case == "reset":
-        al[[0, 7, 30, new[0] - 1]] = 0.0
+        al[[0, 7, min(30, new[0] - 2), new[0] - 1]] = 0.0
     elif case == "keep":
         al[:] = 1.0
         steps = new[0]
@@ -182,7 +184,7 @@ def test_rows_of_others_may_hold_anything(lib):
     import torch
     out = torch.zeros(v.shape, dtype=torch.float16, device="cuda")
     so = torch.zeros(s.shape, dtype=torch.float32, device="cuda")
-    for max_t in (100, 1):
+    for max_t in (100, 1, 32):
         lib.gdn_forward(dev(q), dev(k), dev(v), dev(al), dev(be), dev(cu), dev(s), max_t, state_out=so,
                         out=out)
         torch.cuda.synchronize()
@@ -198,7 +200,7 @@ def test_strided_rows(lib):
     """q, k, v as columns of one fused projection, out as columns of a wider buffer."""
     import torch
     rng = np.random.default_rng(25)
-    for new in ([9, 20], [100, 70]):
+    for new in ([9, 13], [9, 20], [100, 70]):
         q, k, v, al, be, cu, s = inputs(rng, new, 2, 4, 64, np.float16)
         n = len(q)
         want, ws, _ = run(lib, (q, k, v, al, be, cu, s))
@@ -240,7 +242,7 @@ def test_verify_block_then_commit(lib):
         assert np.linalg.norm(host(sd) - s2) <= 1e-4 * np.linalg.norm(s2)
 
 
-@pytest.mark.parametrize("new", [[5, 12], [100, 30]])
+@pytest.mark.parametrize("new", [[5, 12], [21, 40], [100, 30]])
 def test_captured_and_on_another_stream(lib, new):
     """A captured call (state in place) replayed with eager work between equals the eager call each
     time; a call on another stream gives the same bits."""

@@ -7,10 +7,11 @@
 //       = alpha_t S_{t-1} + u_t k_t^T,   u_t = beta_t (v_t - alpha_t S_{t-1} k_t)
 //   o_t = scale S_t q_t                  S [dv x dk], fp32
 //
-// Two forms:
-//   recurrent  token by token with the state in registers (decode, the verify
-//              block, fp32 inputs);
-//   chunked    64 tokens at a time on the matrix cores (prompts).
+// Three forms:
+//   recurrent  token by token with the state in registers (decode, short verify
+//              blocks, fp32 inputs);
+//   block      32 tokens at a time on the matrix cores, one kernel (verify blocks);
+//   chunked    64 tokens at a time on the matrix cores, two kernels (prompts).
 //
 // Recurrent.  A state row needs only itself, k_t and q_t, so a block takes 32
 // rows of one head, 8 threads a row, every thread holding every 8th 16-byte
@@ -244,12 +245,13 @@ __device__ __forceinline__ Pair split(const f32x4& x, const f32x4& y) {
   return p;
 }
 
-// 64 rows of D fp16 from global (row stride ld) into an LDS tile; rows at or past n are zeros
-template <int D, int NT>
+// ROWS rows of D fp16 from global (row stride ld) into an LDS tile, by NT threads; rows at or past n
+// are zeros
+template <int D, int NT, int ROWS = kC>
 __device__ __forceinline__ void stage_rows(_Float16* dst, const _Float16* src, int64_t ld, int n) {
   constexpr int CH = D / 8;
 #pragma unroll
-  for (int u = 0; u < kC * CH / NT; ++u) {
+  for (int u = 0; u < ROWS * CH / NT; ++u) {
     const int e = threadIdx.x + u * NT, r = e / CH, c = e % CH;
     f16x8 x;
 #pragma unroll
@@ -271,6 +273,74 @@ __device__ __forceinline__ void put16(float* C, int ldc, const f32x4& v, float s
   const int col = threadIdx.x & 15, grp = (threadIdx.x & 63) >> 4;
 #pragma unroll
   for (int r = 0; r < 4; ++r) C[(4 * grp + r) * ldc + col] = sign * v[r];
+}
+
+// Products of the gates of 64 tokens, lane t's gate being al (1 behind the last token):
+// s_end[t][k] = prod of alpha over 8 k + 8 .. t, *g = G_t, *d = R[63][t].  By blocks of eight, so
+// that a chain is eleven products long.
+__device__ __forceinline__ void gate_products(float al, float (*s_end)[9], float* g, float* d) {
+  const int lane = threadIdx.x & 63, own = lane >> 3;
+  float up = al, down = 1.f;               // prod over block start .. t, and t + 1 .. block end
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    const float x = __shfl_up(al, i, 64), y = __shfl_down(al, i, 64);
+    if (i <= (lane & 7)) up *= x;
+    if (i <= 7 - (lane & 7)) down *= y;
+  }
+  float v = up;
+#pragma unroll
+  for (int k = 6; k >= -1; --k) {          // block k + 1 whole: its last lane's product
+    const float whole = __shfl(up, 8 * (k + 1) + 7, 64);
+    if (k + 1 < own) v *= whole;
+    if (k >= 0) s_end[lane][k] = k + 1 <= own ? v : 1.f;
+    if (k + 1 > own) down *= whole;
+  }
+  *g = v;
+  *d = down;
+}
+
+// f(e, R[t][i0 + e]) for e = 7 .. 0 (zero where i0 + e > t)
+template <typename F>
+__device__ __forceinline__ void decays(int t, int i0, const float (*s_end)[9], const float* s_alpha,
+                                       F f) {
+  float r = i0 + 8 <= t ? s_end[t][i0 / 8] : 1.f;
+#pragma unroll
+  for (int e = 7; e >= 0; --e) {
+    f(e, i0 + e <= t ? r : 0.f);
+    if (i0 + e <= t) r *= s_alpha[i0 + e];
+  }
+}
+
+// (I + L)^-1 of a 16 x 16 diagonal block by forward substitution, column j by lane j of 16: a row
+// after the other
+__device__ __forceinline__ void invert16(const float* l, float* t, int ld, int j) {
+  float x[16];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    float y = r == j ? 1.f : 0.f;
+#pragma unroll
+    for (int i = 0; i < r; i += 4) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(l + r * ld + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (i + e < r) y = __builtin_fmaf(-v[e], x[i + e], y);
+    }
+    x[r] = y;
+    t[r * ld + j] = y;
+  }
+}
+
+// eight values of a row of T times beta, as a fragment's pair
+__device__ __forceinline__ Pair t_beta(const float* t, const float* beta) {
+  f32x4 x0 = *reinterpret_cast<const f32x4*>(t), x1 = *reinterpret_cast<const f32x4*>(t + 4);
+  const f32x4 b0 = *reinterpret_cast<const f32x4*>(beta);
+  const f32x4 b1 = *reinterpret_cast<const f32x4*>(beta + 4);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x0[e] *= b0[e];
+    x1[e] *= b1[e];
+  }
+  return split(x0, x1);
 }
 
 // One (chunk, head) per block: T diag(beta) and scale R (q.k).  K Q^T and K K^T are
@@ -313,27 +383,11 @@ __global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a, char* __restr
   stage_rows<D, 256>(s_k, static_cast<const _Float16*>(a.k) + row0 * a.ldk + hk * D, a.ldk, n);
   stage_rows<D, 256>(s_q, static_cast<const _Float16*>(a.q) + row0 * a.ldq + hk * D, a.ldq, n);
   if (wave == 0) {
-    // lane t: products of gates from the start of t's block of 8 to t, and on from t to the end
-    // of every block before it: s_end[t][k] = prod of alpha over 8 k + 8 .. t
     const float al = lane < n ? a.alpha[(row0 + lane) * a.H + h] : 1.f;
     s_alpha[lane] = al;
     s_beta[lane] = lane < n ? a.beta[(row0 + lane) * a.H + h] : 0.f;
-    float up = al, down = 1.f;             // prod over block start .. t, and t + 1 .. block end
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-      const float x = __shfl_up(al, i, 64), y = __shfl_down(al, i, 64);
-      if (i <= (lane & 7)) up *= x;
-      if (i <= 7 - (lane & 7)) down *= y;
-    }
-    float v = up;
-#pragma unroll
-    for (int k = 6; k >= -1; --k) {        // block k + 1 whole: its last lane's product
-      const float whole = __shfl(up, 8 * (k + 1) + 7, 64);
-      const int own = lane >> 3;
-      if (k + 1 < own) v *= whole;
-      if (k >= 0) s_end[lane][k] = k + 1 <= own ? v : 1.f;
-      if (k + 1 > own) down *= whole;
-    }
+    float v, down;
+    gate_products(al, s_end, &v, &down);
     float* gate = reinterpret_cast<float*>(out + kOffGate);
     gate[lane] = v;                        // G
     gate[kC + lane] = down;                // R[63][.]
@@ -367,17 +421,13 @@ __global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a, char* __restr
       kk[2 * s] = kk[2 * s + 1] = f32x4{0.f, 0.f, 0.f, 0.f};
       continue;
     }
-    const int i0 = 32 * s + 8 * grp;       // R[t][i0 + 7] .. R[t][i0]
-    float r = i0 + 8 <= t ? s_end[t][i0 / 8] : 1.f;
-#pragma unroll
-    for (int e = 7; e >= 0; --e) {
-      const float d = i0 + e <= t ? r : 0.f;
+    const int i0 = 32 * s + 8 * grp;
+    decays(t, i0, s_end, s_alpha, [&](int e, float d) {
       f32x4& x = kk[2 * s + e / 4];
       f32x4& y = qk[2 * s + e / 4];
       x[e & 3] = i0 + e < t ? bt * d * x[e & 3] : 0.f;
       y[e & 3] = i0 + e <= t ? a.scale * d * y[e & 3] : 0.f;
-      if (i0 + e <= t) r *= s_alpha[i0 + e];
-    }
+    });
     const Pair y = split(qk[2 * s], qk[2 * s + 1]);
     char* f = out + kOffA + (wave < 2 ? wave : 2 * wave - 2 + s) * 2 * kFragBytes + lane * 16;
     *reinterpret_cast<f16x8*>(f) = y.hi;
@@ -395,26 +445,10 @@ __global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a, char* __restr
   }
   __syncthreads();
 
-  // T = (I + L)^-1: the diagonal blocks by forward substitution (lane j: column
-  // j, a row after the other), then the blocks below, one diagonal at a time:
+  // T = (I + L)^-1: the diagonal blocks by forward substitution, then the blocks below, one diagonal at a time:
   // T[i][j] = -T[i][i] sum_{j<=k<i} L[i][k] T[k][j]
   const int o16 = 16 * wave;
-  if (lane < 16) {
-    float x[16];
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      float y = r == lane ? 1.f : 0.f;
-#pragma unroll
-      for (int i = 0; i < r; i += 4) {
-        const f32x4 l = *reinterpret_cast<const f32x4*>(s_l + (o16 + r) * kLd + o16 + i);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (i + e < r) y = __builtin_fmaf(-l[e], x[i + e], y);
-      }
-      x[r] = y;
-      s_t[(o16 + r) * kLd + o16 + lane] = y;
-    }
-  }
+  if (lane < 16) invert16(s_l + o16 * kLd + o16, s_t + o16 * kLd + o16, kLd, lane);
   __syncthreads();
 #pragma unroll
   for (int d = 1; d < 4; ++d) {
@@ -437,19 +471,208 @@ __global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a, char* __restr
   for (int s = 0; s < 2; ++s) {
     if (s > wave / 2) continue;
     const int i0 = 32 * s + 8 * grp;
-    const float* r = s_t + t * kLd + i0;
-    f32x4 x0 = *reinterpret_cast<const f32x4*>(r), x1 = *reinterpret_cast<const f32x4*>(r + 4);
-    const f32x4 b0 = *reinterpret_cast<const f32x4*>(s_beta + i0);
-    const f32x4 b1 = *reinterpret_cast<const f32x4*>(s_beta + i0 + 4);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x0[e] *= b0[e];
-      x1[e] *= b1[e];
-    }
-    const Pair x = split(x0, x1);
+    const Pair x = t_beta(s_t + t * kLd + i0, s_beta + i0);
     char* f = out + (wave < 2 ? wave : 2 * wave - 2 + s) * 2 * kFragBytes + lane * 16;
     *reinterpret_cast<f16x8*>(f) = x.hi;
     *reinterpret_cast<f16x8*>(f + kFragBytes) = x.lo;
+  }
+}
+
+// A short block of positions (the verify's K + 1) in one launch: four waves take a dv tile of 16 state
+// rows each, 32 positions at a time, with the chunked form's products on 32 x 32 systems; a fifth wave
+// makes the gates' products, L and its inverse meanwhile.  What the tiles need besides the state is
+// made once per block of 64 state rows.  Bound by the chain of one pass (loads, gram products,
+// inversion, U, outputs), not by bytes.
+constexpr int kB = 32;
+constexpr int kBLd = kB + 4;
+
+template <int D>
+__global__ __launch_bounds__(320) void gdn_block_kernel(GdnArgs a) {
+  constexpr int DS = D / 32, MT = D / 16;
+  __shared__ __attribute__((aligned(16))) _Float16 s_k[kB * D], s_q[kB * D];
+  __shared__ __attribute__((aligned(16))) float s_l[kB * kBLd], s_t[kB * kBLd];
+  __shared__ float s_m[16 * 17];
+  __shared__ __attribute__((aligned(16))) float s_alpha[64], s_beta[64], s_end[64][9], s_g[64], s_d[64];
+  __shared__ __attribute__((aligned(16))) f16x8 s_ft[2][2][64], s_fa[2][2][64];   // [tile][hi, lo][lane]
+
+  int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = blockIdx.y, b = blockIdx.z, hk = h / (a.H / a.Hk);
+  const Seq sq = seq_of(a, b);
+  const bool solver = wave == 4;
+  const int64_t soff =
+      (((int64_t)b * a.H + h) * D + (blockIdx.x * 4 + wave) * 16 + (lane & 15)) * D + 8 * (lane >> 4);
+  f32x4 st[MT];
+  if (!solver) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      st[m] = *reinterpret_cast<const f32x4*>(a.state + soff + 32 * (m >> 1) + 4 * (m & 1));
+  }
+  for (int t0 = 0; t0 < sq.T; t0 += kB) {
+    // the lane is hidden from the compiler here: offsets made from it anew cost less than the registers
+    // that hold them all over the loop (228 against 128, one block a CU against three)
+    asm volatile("" : "+v"(lane));
+    const int col = lane & 15, grp = lane >> 4;
+    const int dv = (blockIdx.x * 4 + wave) * 16 + col;
+    const auto rows = [&](const _Float16* x, int tt, int s) {
+      const int r = tau(tt, col);
+      return *reinterpret_cast<const f16x8*>(x + r * D + (((4 * s + grp) ^ swz<D>(r)) * 8));
+    };
+    const int n = min(kB, sq.T - t0);
+    const int64_t row0 = sq.start + t0;
+    if (t0 > 0) __syncthreads();           // the previous positions' tiles have been read
+    float v[2][4];
+    if (!solver) {
+      stage_rows<D, 256, kB>(s_k, static_cast<const _Float16*>(a.k) + row0 * a.ldk + hk * D, a.ldk, n);
+      stage_rows<D, 256, kB>(s_q, static_cast<const _Float16*>(a.q) + row0 * a.ldq + hk * D, a.ldq, n);
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = 8 * grp + 4 * tt + r;
+          v[tt][r] = t < n ? (float)static_cast<const _Float16*>(a.v)[(row0 + t) * a.ldv + h * D + dv] : 0.f;
+        }
+    } else {
+      const float al = lane < n ? a.alpha[(row0 + lane) * a.H + h] : 1.f;
+      s_alpha[lane] = al;
+      s_beta[lane] = lane < n ? a.beta[(row0 + lane) * a.H + h] : 0.f;
+      float g, d;
+      gate_products(al, s_end, &g, &d);
+      s_g[lane] = g;
+      s_d[lane] = d;
+    }
+    __syncthreads();
+
+    Pair sp[DS];
+    f32x4 e[2], o[2];
+    if (solver) {
+#pragma unroll
+      for (int ct = 0; ct < 2; ++ct) {
+        f32x4 kk[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int s = 0; s < DS; ++s) {
+          const f16x8 bk = rows(s_k, ct, s);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) kk[i] = mfma16x16x32(rows(s_k, i, s), bk, kk[i]);
+        }
+        const int t = tau(ct, col), i0 = 8 * grp;
+        const float bt = s_beta[t];
+        decays(t, i0, s_end, s_alpha, [&](int x, float d) {
+          kk[x / 4][x & 3] = i0 + x < t ? bt * d * kk[x / 4][x & 3] : 0.f;
+        });
+        float* l = s_l + t * kBLd + i0;
+        *reinterpret_cast<f32x4*>(l) = kk[0];
+        *reinterpret_cast<f32x4*>(l + 4) = kk[1];
+        float* z = s_t + t * kBLd + i0;
+        *reinterpret_cast<f32x4*>(z) = f32x4{0.f, 0.f, 0.f, 0.f};
+        *reinterpret_cast<f32x4*>(z + 4) = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");         // the wave's own tiles
+      if (lane < 32) {
+        const int o16 = (lane & 16) * (kBLd + 1);
+        invert16(s_l + o16, s_t + o16, kBLd, col);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      f32x4 m{0.f, 0.f, 0.f, 0.f};
+      mm16(s_l + 16 * kBLd, kBLd, s_t, kBLd, m);
+      put16(s_m, 17, m, 1.f);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      m = f32x4{0.f, 0.f, 0.f, 0.f};
+      mm16(s_t + 16 * kBLd + 16, kBLd, s_m, 17, m);
+      put16(s_t + 16 * kBLd, kBLd, m, -1.f);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt) {
+        const Pair x = t_beta(s_t + tau(tt, col) * kBLd + 8 * grp, s_beta + 8 * grp);
+        s_ft[tt][0][lane] = x.hi;
+        s_ft[tt][1][lane] = x.lo;
+      }
+    } else {
+      if (wave < 2) {
+        f32x4 qk[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int s = 0; s < DS; ++s) {
+          const f16x8 bq = rows(s_q, wave, s);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) qk[i] = mfma16x16x32(rows(s_k, i, s), bq, qk[i]);
+        }
+        const int t = tau(wave, col), i0 = 8 * grp;
+        decays(t, i0, s_end, s_alpha, [&](int x, float d) {
+          qk[x / 4][x & 3] = i0 + x <= t ? a.scale * d * qk[x / 4][x & 3] : 0.f;
+        });
+        const Pair y = split(qk[0], qk[1]);
+        s_fa[wave][0][lane] = y.hi;
+        s_fa[wave][1][lane] = y.lo;
+      }
+      // X = K S^T (lane: dv, 4 + 4 tokens) and (Q S^T)^T (lane: token, 4 dv)
+#pragma unroll
+      for (int s = 0; s < DS; ++s) sp[s] = split(st[2 * s], st[2 * s + 1]);
+#pragma unroll
+      for (int tt = 0; tt < 2; ++tt) {
+        e[tt] = o[tt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < DS; ++s) {
+          const f16x8 kf = rows(s_k, tt, s), qf = rows(s_q, tt, s);
+          e[tt] = mfma16x16x32(kf, sp[s].hi, e[tt]);
+          e[tt] = mfma16x16x32(kf, sp[s].lo, e[tt]);
+          o[tt] = mfma16x16x32(sp[s].hi, qf, o[tt]);
+          o[tt] = mfma16x16x32(sp[s].lo, qf, o[tt]);
+        }
+        const float g = a.scale * s_g[tau(tt, col)];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          e[tt][r] = v[tt][r] - s_g[8 * grp + 4 * tt + r] * e[tt][r];
+          o[tt][r] *= g;
+        }
+      }
+    }
+    __syncthreads();
+    if (solver) continue;
+
+    const Pair ep = split(e[0], e[1]);
+    f32x4 u[2];
+#pragma unroll
+    for (int tt = 0; tt < 2; ++tt) {
+      const f16x8 th = s_ft[tt][0][lane], tl = s_ft[tt][1][lane];
+      u[tt] = mfma16x16x32(th, ep.hi, f32x4{0.f, 0.f, 0.f, 0.f});
+      u[tt] = mfma16x16x32(tl, ep.hi, u[tt]);
+      u[tt] = mfma16x16x32(th, ep.lo, u[tt]);
+    }
+    Pair up = split(u[0], u[1]);
+    _Float16* out = static_cast<_Float16*>(a.o) + row0 * a.ldo + h * D + (blockIdx.x * 4 + wave) * 16 + 4 * grp;
+#pragma unroll
+    for (int tt = 0; tt < 2; ++tt) {
+      const f16x8 ah = s_fa[tt][0][lane], al = s_fa[tt][1][lane];
+      o[tt] = mfma16x16x32(up.hi, ah, o[tt]);
+      o[tt] = mfma16x16x32(up.hi, al, o[tt]);
+      o[tt] = mfma16x16x32(up.lo, ah, o[tt]);
+      const int t = tau(tt, col);
+      if (t < n)
+        *reinterpret_cast<f16x4*>(out + t * a.ldo) = f16x4{(_Float16)o[tt][0], (_Float16)o[tt][1],
+                                                           (_Float16)o[tt][2], (_Float16)o[tt][3]};
+    }
+    if (a.state_out == nullptr && t0 + kB >= sq.T) break;
+#pragma unroll
+    for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) u[tt][r] *= s_d[8 * grp + 4 * tt + r];
+    up = split(u[0], u[1]);
+    const float gc = s_g[63];
+    const int tr = 8 * grp + (col >> 2);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) st[m][r] *= gc;
+      // rows rho of tile m are dk 32 (m / 2) + 8 (rho / 4) + 4 (m & 1) + rho % 4
+      const uint32_t k = lds_addr(s_k) + tr * D * 2 + ((4 * (m >> 1) + (col & 3)) ^ swz<D>(tr)) * 16 + 8 * (m & 1);
+      const f16x8 kt = join8(lds_get_tr(k), lds_get_tr(k + 4 * D * 2));
+      st[m] = mfma16x16x32(kt, up.hi, st[m]);
+      st[m] = mfma16x16x32(kt, up.lo, st[m]);
+    }
+  }
+  if (a.state_out != nullptr && !solver) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      *reinterpret_cast<f32x4*>(a.state_out + soff + 32 * (m >> 1) + 4 * (m & 1)) = st[m];
   }
 }
 
@@ -790,7 +1013,17 @@ size_t gdn_forward_workspace(const GdnPlan& p, int N, int B, int H) {
   return p.chunked ? kTicketRegion + ((size_t)(N / kC) + B) * H * kSlotBytes : 0;
 }
 
-GdnPlan plan_gdn(int N, int max_t, int f32) { return GdnPlan{N > 0 && !f32 && max_t > 64}; }
+// The form by the longest sequence (fp16; fp32 goes one by one).  Times in us of one by one / 32 at a
+// time / 64 at a time, 16 heads of 128, B sequences:
+//   B = 1    T = 8  6.0 /  8.4 / 12.5    16  8.7 /  8.6 / 12.5   32  15 /  8.7 / 12.6   96  - / 18.5 / 14.5
+//   B = 8    T = 8  7.8 /  9.6 / 19.5    16 11.1 /  9.8 / 19.5   32  19 / 10.0 / 19.6   64 35 / 15.4 / 21
+//   B = 64   T = 8   35 /   62 / 84      16   55 /   66 / 84     32  98 /   72 / 87     64 185 / 126 / 108
+GdnPlan plan_gdn(int N, int max_t, int f32) {
+  GdnPlan p;
+  p.chunked = N > 0 && !f32 && max_t > 64;
+  p.block = !p.chunked && !f32 && max_t > 16;
+  return p;
+}
 
 template <int D, int NV>
 static void launch_scan(const GdnArgs& a, const void* ws, hipStream_t stream) {
@@ -811,6 +1044,8 @@ static void launch_gdn(const GdnArgs& a, const GdnPlan& p, void* ws, hipStream_t
     // 70 / 57, 123 / 100 us.
     if ((int64_t)a.B * a.H * (D / 16) <= 256) launch_scan<D, 1>(a, ws, stream);
     else launch_scan<D, 2>(a, ws, stream);
+  } else if (p.block) {
+    hipLaunchKernelGGL(gdn_block_kernel<D>, dim3(D / 64, a.H, a.B), dim3(320), 0, stream, a);
   } else if (a.f32) {
     hipLaunchKernelGGL((gdn_recurrent_kernel<D, float>), dim3(D / kRows, a.H, a.B), dim3(kThreads), 0,
                        stream, a);

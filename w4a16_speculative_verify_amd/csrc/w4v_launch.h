@@ -222,7 +222,8 @@ struct GdnArgs {
   int N, B, Hk, H, D, f32;
 };
 struct GdnPlan {
-  bool chunked;
+  bool chunked;      // 64 positions at a time, two kernels
+  bool block;        // else 32 at a time in one kernel (or one by one)
 };
 GdnPlan plan_gdn(int N, int max_t, int f32);
 size_t gdn_forward_workspace(const GdnPlan& p, int N, int B, int H);
