@@ -117,6 +117,35 @@ def test_unused_places_may_hold_anything(lib):
         assert np.array_equal(got, clean)
 
 
+@pytest.mark.parametrize("new,d", [(2, 128), (2, 256), (12, 64), (20, 128), (40, 128), (100, 64), (50, 256)])
+def test_later_positions_may_hold_anything(lib, new, d):
+    """NaN and infinities in the keys and values of the last positions of a chunk: the rows before
+    them are bit for bit what they are without, the rows that see an infinity or NaN give it."""
+    rng = np.random.default_rng(new + d)
+    x = gen.paged_batch(rng, [new, 1], [new + 37, 9], 4, 2, d, 16)
+    clean, _ = run_attention(lib, x)
+    kinds = [np.inf, -np.inf, np.nan]
+    for i in range(min(3, new)):
+        p = new + 36 - i                                      # the last positions, from the end
+        x.v_cache[x.table[0, p // 16], :, p % 16, i::7] = kinds[i]
+    p = new + 36
+    args = [dev(a) for a in (x.q, x.k_cache, x.v_cache, x.table, x.cu, x.ctx)]
+    got = host(lib.paged_attention(*args, x.max_q))
+    first = max(0, new - 3)                                   # first row that sees one
+    assert np.array_equal(got[:first], clean[:first]) and np.array_equal(got[new:], clean[new:])
+    ref, _, _, _ = oa.attention(x.q, x.k_cache, x.v_cache, x.table, x.cu, x.ctx, d ** -0.5)
+    want = ref[first:new]
+    assert np.array_equal(np.isnan(got[first:new]), np.isnan(want))
+    inf = np.isinf(want)
+    assert np.array_equal(got[first:new][inf].astype(np.float64), want[inf])
+    assert np.all(np.isfinite(got[first:new][np.isfinite(want)]))
+    x.k_cache[x.table[0, p // 16], :, p % 16] = np.nan         # and keys: the last row alone
+    args[1] = dev(x.k_cache)
+    got = host(lib.paged_attention(*args, x.max_q))
+    assert np.array_equal(got[:first], clean[:first]) and np.all(np.isnan(got[new - 1]))
+    assert np.all(np.isfinite(got[new:]))
+
+
 def test_pages_outside_the_cache_are_not_seen(lib):
     """Entries inside the context that point nowhere, and a context longer than its table."""
     rng = np.random.default_rng(5)

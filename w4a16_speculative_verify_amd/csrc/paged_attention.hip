@@ -11,6 +11,7 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr uint32_t kRing = 128 * 1024;     // LDS: the waves' key/value rings, then the merge
+constexpr size_t kJoinStride = 16;         // words between two row tiles' counters: 1,024 of them
 constexpr float kLazy = 8.0f;              // running maxima move once a score exceeds them by 2^8
 
 // keys per tile and tiles in flight of one wave's ring: 32 KiB per wave
@@ -33,6 +34,30 @@ __device__ __forceinline__ int swz_k(int r) {
 template <int D>
 __device__ __forceinline__ int swz_v(int r) {
   return D == 64 ? ((r >> 1) & 3) * 2 : (2 * r) & 15;
+}
+
+// Values that are not finite, at keys that some rows of a tile see and others do not (a later
+// position's place in the cache may hold anything): a weight of zero does not hide them from a matrix
+// product.  Tiles with hidden keys are looked through; such values become zeros in LDS, and the rows
+// that do see the key get them added from memory after the product.
+__device__ __forceinline__ uint32_t not_finite2(uint32_t x) {      // bit 0 / 16: low / high half
+  return (((x & 0x7c007c00u) + 0x04000400u) >> 15) & 0x00010001u;
+}
+// zeroes them in the 16 bytes of LDS at off; whether there were any
+__device__ __forceinline__ bool clean16(uint32_t off) {
+  u32x4 x = lds_get<u32x4>(off);
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t bad = not_finite2(x[i]);
+    x[i] &= ~(bad * 0xffffu);
+    any |= bad;
+  }
+  if (any) lds_put(off, x);
+  return any != 0;
+}
+__device__ __forceinline__ float only_not_finite(_Float16 v) {
+  return fabsf((float)v) <= 65504.f ? 0.f : (float)v;
 }
 
 // the larger (or the sum) of the two lanes that hold one column of a 32 x 32 tile
@@ -110,18 +135,6 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
   const int t_hi = (int)((int64_t)nt * (split + 1) / splits);
   const int all_see = sq.p0 + row0 / G;                        // keys up to here every row sees
 
-  f16x8 q[RT][DS];
-  int lim[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int x = min(row0 + 16 * rt + col, nrows - 1);
-    const int i = x / G, g = x % G;
-    lim[rt] = min(sq.p0 + i, sq.len - 1);
-    const _Float16* p = a.q + (int64_t)(sq.start + i) * a.ldq + (h * G + g) * D + 8 * grp;
-#pragma unroll
-    for (int s = 0; s < DS; ++s) q[rt][s] = *reinterpret_cast<const f16x8*>(p + 32 * s);
-  }
-
   // DMA source offsets of this lane inside a group: LDS chunk position -> chunk
   uint32_t ko[L::kDma], vo[L::kDma];
 #pragma unroll
@@ -133,18 +146,28 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
   const uint32_t ring = lds_addr(s_ring) + wave * (kRing / kWaves);
   const int32_t* table = a.table + (int64_t)b * a.max_pages;
 
-  // page of group gi of tile t (-1 behind the end)
-  const auto page_of = [&](int t, int gi) -> int {
-    const int key = t * L::KT + 16 * gi;
-    if (t >= t_hi || key >= end) return -1;
+  const auto page_of = [&](int key) -> int {
+    if (key >= end) return -1;
     const int p = table[key >> a.page_shift];
     return (unsigned)p < (unsigned)a.num_pages ? p : -1;
   };
-  const auto issue = [&](int t, int slot, const int* pages) {
+  // lane j: the page of group j % NG of the wave's (pages_at + j / NG)-th tile, so that the table is
+  // read once in 64 / NG tiles and a tile's pages cost no wait; bad: one of them lies outside the cache,
+  // and from there on tiles are looked at key by key also where every row sees them whole
+  const int t0 = t_lo + wave;
+  int pages = -1, pages_at = -64;
+  bool bad = false;
+  const auto issue = [&](int i, int slot) {            // the wave's i-th tile
+    if (i - pages_at >= 64 / NG) {
+      pages_at = i;
+      const int t = t0 + (i + lane / NG) * kWaves, key = t * L::KT + 16 * (lane % NG);
+      pages = t < t_hi ? page_of(key) : -1;
+      bad |= __any(t < t_hi && key < end && pages < 0) != 0;
+    }
 #pragma unroll
     for (int gi = 0; gi < NG; ++gi) {
-      const int key = t * L::KT + 16 * gi;
-      const int pg = pages[gi];
+      const int key = (t0 + i * kWaves) * L::KT + 16 * gi;
+      const int pg = __builtin_amdgcn_readlane(pages, (i - pages_at) * NG + gi);
       const int64_t off =
           pg < 0 ? 0 : (((int64_t)pg * a.Hkv + h) * a.page_size + (key & (a.page_size - 1))) * D;
       const uint32_t bytes = pg < 0 ? 0u : (uint32_t)min(16, end - key) * (D * 2);
@@ -157,6 +180,20 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
       }
     }
   };
+#pragma unroll
+  for (int s = 0; s < L::NS; ++s) issue(s, s);
+
+  f16x8 q[RT][DS];
+  int lim[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const int x = min(row0 + 16 * rt + col, nrows - 1);
+    const int i = x / G, g = x % G;
+    lim[rt] = min(sq.p0 + i, sq.len - 1);
+    const _Float16* p = a.q + (int64_t)(sq.start + i) * a.ldq + (h * G + g) * D + 8 * grp;
+#pragma unroll
+    for (int s = 0; s < DS; ++s) q[rt][s] = *reinterpret_cast<const f16x8*>(p + 32 * s);
+  }
 
   f32x4 o[RT][DT];
   float m[RT], l[RT];
@@ -167,17 +204,6 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[rt][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-
-  int pg[L::NS][NG], pn[NG];
-  const int t0 = t_lo + wave;
-#pragma unroll
-  for (int s = 0; s < L::NS; ++s) {
-#pragma unroll
-    for (int gi = 0; gi < NG; ++gi) pg[s][gi] = page_of(t0 + s * kWaves, gi);
-    issue(t0 + s * kWaves, s, pg[s]);
-  }
-#pragma unroll
-  for (int gi = 0; gi < NG; ++gi) pn[gi] = page_of(t0 + L::NS * kWaves, gi);
 
   const float c = a.scale * 1.44269504088896341f;
   // lane offsets of the operand reads
@@ -192,7 +218,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
     va[d] = (uint32_t)(vkey * D * 2 + ((2 * d + (col & 3) / 2) ^ swz_v<D>(vkey)) * 16 + (col & 1) * 8);
 
   int slot = 0;
-  for (int t = t0; t < t_hi; t += kWaves) {
+  for (int i = 0, t = t0; t < t_hi; ++i, t += kWaves) {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"((L::NS - 1) * L::kPer) : "memory");
     const uint32_t kb = ring + slot * L::kTile, vb = kb + NG * L::kGroup;
 
@@ -208,12 +234,24 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
         for (int rt = 0; rt < RT; ++rt) sc[rt][gi] = mfma16x16x32(k, q[rt][s], sc[rt][gi]);
       }
     }
-    bool hide = t * L::KT + L::KT - 1 > all_see;
+    const bool hide = bad || t * L::KT + L::KT - 1 > all_see;
+    bool ok[NG];
 #pragma unroll
-    for (int gi = 0; gi < NG; ++gi) hide |= pg[0][gi] < 0;
+    for (int gi = 0; gi < NG; ++gi) ok[gi] = !bad || page_of(t * L::KT + 16 * gi) >= 0;
+    uint32_t dirty = 0;                    // keys with values that are not finite
+    if (hide) {
+      constexpr int LR = D / 8;            // lanes a row
+#pragma unroll
+      for (int u = 0; u < (int)(NG * L::kGroup / 1024); ++u) {
+        const uint64_t found = __ballot(clean16(vb + u * 1024 + lane * 16));
+#pragma unroll
+        for (int r = 0; r < 64 / LR; ++r)
+          if ((found >> (r * LR)) & ((1ull << LR) - 1)) dirty |= 1u << (u * (64 / LR) + r);
+      }
+    }
 
-    f16x8 p[RT];
-    f16x4 p4[RT];
+    f16x8 p[RT][2];                        // the weights as pairs of fp16, p + the remainder
+    f16x4 p4[RT][2];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       float mx = -INFINITY;
@@ -224,7 +262,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
           float v = sc[rt][gi][r] * c;
           if (hide) {
             const int key = t * L::KT + 16 * gi + 4 * grp + r;
-            v = key <= lim[rt] && pg[0][gi] >= 0 ? v : -INFINITY;
+            v = key <= lim[rt] && ok[gi] ? v : -INFINITY;
           }
           sc[rt][gi][r] = v;
           mx = fmaxf(mx, v);
@@ -245,10 +283,17 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
       for (int gi = 0; gi < NG; ++gi)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float e = __builtin_amdgcn_exp2f(sc[rt][gi][r] - mu);
+          float e = __builtin_amdgcn_exp2f(sc[rt][gi][r] - mu);
+          asm("" : "+v"(e));               // one value for both halves of the pair
           l[rt] += e;
-          if constexpr (NG == 2) p[rt][4 * gi + r] = (_Float16)e;
-          else p4[rt][r] = (_Float16)e;
+          const _Float16 eh = (_Float16)e, el = (_Float16)(e - (float)eh);
+          if constexpr (NG == 2) {
+            p[rt][0][4 * gi + r] = eh;
+            p[rt][1][4 * gi + r] = el;
+          } else {
+            p4[rt][0][r] = eh;
+            p4[rt][1][r] = el;
+          }
         }
     }
 #pragma unroll
@@ -256,26 +301,36 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
       if constexpr (NG == 2) {
         const f16x8 v = join8(lds_get_tr(vb + va[d]), lds_get_tr(vb + L::kGroup + va[d]));
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) o[rt][d] = mfma16x16x32(v, p[rt], o[rt][d]);
+        for (int rt = 0; rt < RT; ++rt) {
+          o[rt][d] = mfma16x16x32(v, p[rt][0], o[rt][d]);
+          o[rt][d] = mfma16x16x32(v, p[rt][1], o[rt][d]);
+        }
       } else {
         const f16x4 v = lds_get_tr(vb + va[d]);
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-          o[rt][d] = __builtin_amdgcn_mfma_f32_16x16x16f16(v, p4[rt], o[rt][d], 0, 0, 0);
+        for (int rt = 0; rt < RT; ++rt) {
+          o[rt][d] = __builtin_amdgcn_mfma_f32_16x16x16f16(v, p4[rt][0], o[rt][d], 0, 0, 0);
+          o[rt][d] = __builtin_amdgcn_mfma_f32_16x16x16f16(v, p4[rt][1], o[rt][d], 0, 0, 0);
+        }
       }
+    }
+    for (; dirty != 0; dirty &= dirty - 1) {
+      const int key = t * L::KT + (int)__builtin_ctz(dirty), pg = page_of(key);
+      if (pg < 0) continue;
+      const _Float16* v = a.v_cache +
+          (((int64_t)pg * a.Hkv + h) * a.page_size + (key & (a.page_size - 1))) * D + 4 * grp;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float x = only_not_finite(v[16 * d + r]);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) o[rt][d][r] += key <= lim[rt] ? x : 0.f;
+        }
     }
     // the slot's reads are done: refill it
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    issue(t + L::NS * kWaves, slot, pn);
-#pragma unroll
-    for (int s = 0; s + 1 < L::NS; ++s)
-#pragma unroll
-      for (int gi = 0; gi < NG; ++gi) pg[s][gi] = pg[s + 1][gi];
-#pragma unroll
-    for (int gi = 0; gi < NG; ++gi) {
-      pg[L::NS - 1][gi] = pn[gi];
-      pn[gi] = page_of(t + (L::NS + 1) * kWaves, gi);
-    }
+    issue(i + L::NS, slot);
     slot = slot + 1 == L::NS ? 0 : slot + 1;
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no copy lands in the ring any more
@@ -332,7 +387,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
   }
   if (splits == 1 || tickets == nullptr) return;
   // ---- the block that arrives last joins the splits, in their order
-  if (!arrive_last(tickets + item * kTicketStride, splits)) return;
+  if (!arrive_last(tickets + item * kJoinStride, splits)) return;
   const rsrc_t po = make_rsrc(part + item * splits * R * (D + 2));
   const uint32_t step = (uint32_t)(R * (D + 2)) * 4;
   for (int i = tid; i < R * (D / 4); i += kThreads) {
@@ -409,6 +464,7 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
   using L = TileRing<D, NW>;
   constexpr int DT = D / 32, DS = D / 16, NSub = L::NSub, kTileRows = L::kRows;
   __shared__ __attribute__((aligned(1024))) unsigned char s_ring[L::NS * 2 * L::kHalf];
+  __shared__ unsigned long long s_dirty[2];            // keys of a tile with values that are not finite
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
@@ -424,11 +480,10 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
   const int t_lo = (int)((int64_t)nt * split / splits);
   const int t_hi = (int)((int64_t)nt * (split + 1) / splits);
 
-  // the wave's rows: keys up to all_see every row sees, behind any_see none
+  // the wave's rows: behind any_see none sees a key
   const int wr0 = row0 + 32 * wave;
   const int x = min(wr0 + col, nrows - 1), xi = x / G, xg = x % G;
   const int lim = min(sq.p0 + xi, sq.len - 1);
-  const int all_see = sq.p0 + min(wr0, nrows - 1) / G;
   const int any_see = wr0 < nrows ? sq.p0 + min(wr0 + 31, nrows - 1) / G : -1;
 
   uint32_t ko[L::kDma], vo[L::kDma];       // source offsets of the lane's chunks
@@ -468,6 +523,14 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
       dma16(dst + L::kHalf + u * 1024, rv, vo[u]);
     }
   };
+  // whether any page of the block's keys lies outside the cache: only then tiles that every row
+  // sees are looked at key by key
+  if (threadIdx.x < 2) s_dirty[threadIdx.x] = 0;
+  bool bad = false;
+  for (int k = t_lo * L::KT + 16 * (int)threadIdx.x; k < min(t_hi * L::KT, end);
+       k += 16 * 64 * NW)
+    bad |= page_of(k) < 0;
+  bad = __syncthreads_or(bad);
 #pragma unroll
   for (int s = 0; s + 1 < L::NS; ++s) issue(t_lo + s, s);
 
@@ -477,14 +540,6 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
 #pragma unroll
     for (int s = 0; s < DS; ++s) q[s] = *reinterpret_cast<const f16x8*>(p + 16 * s);
   }
-
-  // whether any page of the block's keys lies outside the cache: only then tiles that every row
-  // sees are looked at key by key
-  bool bad = false;
-  for (int k = t_lo * L::KT + 16 * (int)threadIdx.x; k < min(t_hi * L::KT, end);
-       k += 16 * 64 * NW)
-    bad |= page_of(k) < 0;
-  bad = __syncthreads_or(bad);
 
   f32x16 o[DT];
 #pragma unroll
@@ -506,6 +561,9 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
             ((4 * d + 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1)) ^ tswz_v<D>(vkey)) * 16;
 
   int slot = 0;
+  // tiles up to clear every row of the block sees whole; the others (the last one or two of a causal
+  // context) pay for the masks
+  const int clear = bad ? t_lo : (sq.p0 + row0 / G + 1) / L::KT;
   for (int t = t_lo; t < t_hi; ++t) {
     // tile t has landed, and every wave is done with tile t - 1, whose place the next copy takes
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"((L::NS - 2) * 2 * L::kDma) : "memory");
@@ -514,6 +572,17 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
     const uint32_t so = slot * 2 * L::kHalf;
     slot = slot + 1 == L::NS ? 0 : slot + 1;
     const int key0 = t * L::KT;
+    const bool hide = t >= clear;
+    if (hide) {
+      // each wave looks through the values that it copied
+      if (threadIdx.x == 0) s_dirty[(t + 1) & 1] = 0;
+#pragma unroll
+      for (int u = 0; u < L::kDma; ++u) {
+        const uint32_t at = wave * (L::KW * D * 2) + u * 1024 + lane * 16;
+        if (clean16(ring + L::kHalf + so + at)) atomicOr(&s_dirty[t & 1], 1ull << (at / (D * 2)));
+      }
+      lds_barrier();
+    }
     if (key0 > any_see) continue;          // none of the wave's rows sees the tile
 
     f32x16 sc[NSub];
@@ -527,8 +596,8 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
         sc[j] = mfma32x32x16(k, q[s], sc[j]);
       }
     }
-    if (bad || key0 + L::KT - 1 > all_see) {
-      uint32_t ok = (1u << L::NG) - 1;
+    uint32_t ok = (1u << L::NG) - 1;
+    if (hide) {
       if (bad) {
         ok = 0;
 #pragma unroll
@@ -579,6 +648,18 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
           const uint32_t v = va[d] + so + (32 * j + 16 * s) * D * 2;
           o[d] = mfma32x32x16(join8(lds_get_tr(v), lds_get_tr(v + 8 * D * 2)), p[s], o[d]);
         }
+    }
+    if (hide) {
+      for (uint64_t left = s_dirty[t & 1]; left != 0; left &= left - 1) {
+        const int key = key0 + (int)__builtin_ctzll(left), pg = page_of(key);
+        if (pg < 0 || key > lim) continue;
+        const _Float16* v = a.v_cache +
+            (((int64_t)pg * a.Hkv + h) * a.page_size + (key & (a.page_size - 1))) * D + 4 * half;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[d][r] += only_not_finite(v[32 * d + 8 * (r / 4) + r % 4]);
+      }
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -713,11 +794,19 @@ AttnPlan plan_attention(int B, int max_q, int max_ctx, int Hq, int Hkv, int D) {
   p.row_tiles = (int)((rows + p.rows - 1) / p.rows);
   const int64_t items = (int64_t)B * Hkv * p.row_tiles;
   const int tiles = (max_ctx + 31) / 32;
-  const int blocks = p.rows <= 32 || (p.rows == 256 && D == 128) ? 256 : 512;   // that the CUs hold
-  p.splits = 1;
-  if (items < blocks)
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({64, blocks / items, tiles / 8}));
-  p.last_joins = p.rows <= 32 && std::min<int64_t>(rows, p.rows) * p.splits <= 128;
+  // Blocks that the CUs hold at a time: while there are fewer row tiles, contexts are split, down to 8
+  // tiles of 32 keys a block.  (One token a sequence, 8 key heads, us at 256 / 512 / 1,024 blocks: 4
+  // sequences of 8,192 tokens 27 / 32 / 48, 16 of 16,384 188 / 190 / 196; splits of 16 or 32 tiles and
+  // more: 1 of 1,001 tokens 11 and 13.5 against 8.9, 1 of 8,208 14 and 18 against 13.)
+  const int blocks = p.rows <= 32 || (p.rows == 256 && D == 128) ? 256 : 512;
+  int64_t splits = items < blocks ? std::min<int64_t>(blocks / items, tiles / 8) : 1;
+  // Many long sequences, seldom of one length: splits of 128 tiles and more, up to 2,048 blocks, even
+  // out what the CUs get (64 ragged sequences up to 16,384 tokens 527 -> 480 us; shorter splits cost
+  // more than they give, 64 of 2,048 tokens 98 unsplit, 110 in two).
+  if (p.rows <= 32 && items >= blocks) splits = std::min<int64_t>(2048 / items, tiles / 128);
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(64, splits));
+  p.last_joins = p.rows <= 32 && std::min<int64_t>(rows, p.rows) * p.splits <= 128 &&
+                 items * kJoinStride * sizeof(unsigned) <= kTicketRegion;
   p.workspace = p.splits == 1 ? 0 : kTicketRegion + (size_t)items * p.splits * p.rows * (D + 2) * sizeof(float);
   return p;
 }
