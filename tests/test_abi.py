@@ -492,3 +492,19 @@ def test_gdn_forward_workspace(lib):
     need = size(100, 2, 100, 16, 16, 128, torch.float16)
     assert gdn(lib, max_t=100, wsb=need - 1) == WORKSPACE
     assert gdn(lib, max_t=100, ws=A + 16) == ALIGN
+
+
+def test_new_calls_refuse_host_tensors():
+    """A tensor in host memory never reaches the library as a device address."""
+    import torch
+    f, i = torch.float16, torch.int32
+    kc = torch.zeros((2, 1, 16, 64), dtype=f)
+    table, cu, ctx = torch.zeros((1, 1), dtype=i), torch.tensor([0, 1], dtype=i), torch.ones(1, dtype=i)
+    qkv, inv = torch.zeros((1, 192), dtype=f), torch.ones(32)
+    with pytest.raises(ValueError):
+        w4v.rope_kv_append(qkv, kc, kc.clone(), table, cu, ctx, inv, 1)
+    with pytest.raises(ValueError):
+        w4v.paged_attention(torch.zeros((1, 1, 64), dtype=f), kc, kc, table, cu, ctx, 1)
+    x, g = torch.zeros((1, 1, 64)), torch.ones((1, 1))
+    with pytest.raises(ValueError):
+        w4v.gdn_forward(x, x, x, g, g, cu, torch.zeros((1, 1, 64, 64)), 1)

@@ -482,28 +482,33 @@ def _elsewhere(t, stream):
     """Whether a call has to enter another device or stream first (its own allocations then belong
     to that stream)."""
     import torch
+    if not t.is_cuda:
+        raise ValueError("the tensors must be on a GPU")
     if stream is not None:
         if stream.device != t.device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
         return True
-    return t.is_cuda and t.device.index != torch.cuda.current_device()
+    return t.device.index != torch.cuda.current_device()
 
 
 def _whole(t, dtype, device, name):
     """A contiguous tensor of this type on this device."""
     if t.dtype is not dtype or t.device != device or not t.is_contiguous():
-        _require(t, dtype, name)
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+        _refuse(t, dtype, device, name)
         raise ValueError(f"{name} must be contiguous")
+
+
+def _refuse(t, dtype, device, name):
+    _require(t, dtype, name)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 def _rows(t, dtype, device, name, n, heads, d):
     """[n, heads, d] (or [n, heads * d]) of this type on this device, a row's heads contiguous, rows
     at any stride; returns the row stride (the width for a single row, whose stride says nothing)."""
     if t.dtype is not dtype or t.device != device:
-        _require(t, dtype, name)
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+        _refuse(t, dtype, device, name)
     shape, stride = t.shape, t.stride()
     if len(shape) == 3:
         ok = shape == (n, heads, d) and (n == 0 or (stride[2] == 1 and
@@ -519,11 +524,16 @@ def _rows(t, dtype, device, name, n, heads, d):
 def _paged(k_cache, v_cache, block_table, cu, ctx_lens, device):
     """(pages, kv heads, page size, head width, sequences) of a paged cache and its batch."""
     import torch
-    _whole(k_cache, torch.float16, device, "k_cache")
-    _whole(v_cache, torch.float16, device, "v_cache")
-    _whole(block_table, torch.int32, device, "block_table")
-    _whole(cu, torch.int32, device, "cu")
-    _whole(ctx_lens, torch.int32, device, "ctx_lens")
+    f16, i32 = torch.float16, torch.int32
+    if not (k_cache.dtype is f16 and v_cache.dtype is f16 and block_table.dtype is i32 and
+            cu.dtype is i32 and ctx_lens.dtype is i32 and k_cache.is_contiguous() and
+            v_cache.is_contiguous() and block_table.is_contiguous() and cu.is_contiguous() and
+            ctx_lens.is_contiguous() and k_cache.device == device and v_cache.device == device and
+            block_table.device == device and cu.device == device and ctx_lens.device == device):
+        for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            _whole(t, f16, device, name)
+        for t, name in ((block_table, "block_table"), (cu, "cu"), (ctx_lens, "ctx_lens")):
+            _whole(t, i32, device, name)
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must both be [pages, kv heads, page size, D]")
@@ -601,7 +611,8 @@ def rope_kv_append(qkv, k_cache, v_cache, block_table, cu, ctx_lens, inv_freq, h
             return rope_kv_append(qkv, k_cache, v_cache, block_table, cu, ctx_lens, inv_freq, hq,
                                   interleaved, mscale, q_out)
     dev = qkv.device
-    _require(qkv, torch.float16, "qkv")
+    if qkv.dtype is not torch.float16 or not qkv.is_cuda or qkv.stride(-1) != 1:
+        _require(qkv, torch.float16, "qkv")
     pages, hkv, page, d, b = _paged(k_cache, v_cache, block_table, cu, ctx_lens, dev)
     _whole(inv_freq, torch.float32, dev, "inv_freq")
     width = (hq + 2 * hkv) * d
@@ -609,7 +620,7 @@ def rope_kv_append(qkv, k_cache, v_cache, block_table, cu, ctx_lens, inv_freq, h
         raise ValueError(f"qkv must be [N, >= {width}], got {tuple(qkv.shape)}")
     n = qkv.shape[0]
     if q_out is None:
-        q_out = torch.empty((n, hq, d), dtype=torch.float16, device=dev)
+        q_out = qkv.new_empty((n, hq, d))
     ldq = _rows(q_out, torch.float16, dev, "q_out", n, hq, d)
     st = load().rope_kv_append(
         qkv.data_ptr(), qkv.stride(0) if n > 1 else width, q_out.data_ptr(), ldq,
@@ -648,7 +659,7 @@ def paged_attention(q, k_cache, v_cache, block_table, cu, ctx_lens, max_q: int, 
     n, hq = q.shape[0], q.shape[1]
     ldq = _rows(q, torch.float16, dev, "q", n, hq, d)
     if out is None:
-        out = torch.empty((n, hq, d), dtype=torch.float16, device=dev)
+        out = q.new_empty((n, hq, d))
     ldo = _rows(out, torch.float16, dev, "out", n, hq, d)
     if max_ctx is None:
         max_ctx = min(block_table.shape[1] * page, 2**31 - 1)
@@ -711,7 +722,7 @@ def gdn_forward(q, k, v, alpha, beta, cu, state, max_t: int, state_out=None, sca
             raise ValueError("state_out must have state's shape")
         so = state_out.data_ptr()
     if out is None:
-        out = torch.empty((n, h, d), dtype=dt, device=dev)
+        out = q.new_empty((n, h, d))
     ldo = _rows(out, dt, dev, "out", n, h, d)
     lib = load()
     f32 = dt is torch.float32
