@@ -687,8 +687,8 @@ __global__ __launch_bounds__(320) void gdn_block_kernel(GdnArgs a) {
 // copies the next chunk's K, Q, V rows and fragments into the other half of a
 // double buffer (LDS DMA), so that nothing waits for memory inside a chunk.
 // Three barriers a chunk:
-//   1  the chunk's copies have landed, S is in LDS
-//   2  the halves' X of the other's tokens are in LDS
+//   1  the chunk's copies but A have landed, S is in LDS
+//   2  A has landed, the halves' X of the other's tokens are in LDS
 //   3  U is in LDS: that of tokens 0 .. 31, and of 32 .. 63 in two addends (and
 //      the output wave is done with S)
 template <int D, int NV>
@@ -743,24 +743,25 @@ __global__ __launch_bounds__(64 * (3 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
   if (wave == 3 * NV) {
     // ---- the copying wave
     constexpr int CH = D / 8, CV = 2 * NV;
-    const auto copy = [&](int c, int part) {   // part 0: K and V, T and the gates; part 1: Q, A
+    // part 0: K, V and the gates; part 1: Q and T; part 2: A, which is read last
+    constexpr int kPart0 = CH + CV + 1, kPart2 = kOffA / 1024;
+    const auto copy = [&](int c, int part) {
       const uint32_t dst = lds + (c & 1) * L::kBuf;
       const int n = min(kC, sq.T - c * kC);
       const int64_t row0 = sq.start + (int64_t)c * kC;
       // rows at or past n lie behind the resource's end and become zeros
       const u32x4s rf = dma_rsrc(ws + ((int64_t)(slot0 + c) * a.H + h) * kSlotBytes, kSlotBytes);
-      const int64_t ld = part == 0 ? a.ldk : a.ldq;
-      const auto* x = static_cast<const _Float16*>(part == 0 ? a.k : a.q) + row0 * ld + hk * D;
-      const u32x4s rx = dma_rsrc(x, (uint32_t)((n - 1) * (int)ld + D) * 2);
-      const uint32_t to = dst + (part == 0 ? 0u : L::kQ), ff = part * kOffA;
+      if (part < 2) {
+        const int64_t ld = part == 0 ? a.ldk : a.ldq;
+        const auto* x = static_cast<const _Float16*>(part == 0 ? a.k : a.q) + row0 * ld + hk * D;
+        const u32x4s rx = dma_rsrc(x, (uint32_t)((n - 1) * (int)ld + D) * 2);
+        const uint32_t to = dst + (part == 0 ? 0u : L::kQ);
 #pragma unroll
-      for (int u = 0; u < CH; ++u) {
-        const int e = u * 64 + lane, r = e / CH, ch = (e % CH) ^ swz<D>(r);
-        dma16(to + u * 1024, rx, (uint32_t)(r * (int)ld * 2 + ch * 16));
+        for (int u = 0; u < CH; ++u) {
+          const int e = u * 64 + lane, r = e / CH, ch = (e % CH) ^ swz<D>(r);
+          dma16(to + u * 1024, rx, (uint32_t)(r * (int)ld * 2 + ch * 16));
+        }
       }
-#pragma unroll
-      for (int u = 0; u < kOffA / 1024; ++u)
-        dma16(dst + L::kF + ff + u * 1024, rf, ff + u * 1024 + lane * 16);
       if (part == 0) {
         const auto* v = static_cast<const _Float16*>(a.v) + row0 * a.ldv + h * D + dv0;
         const u32x4s rv = dma_rsrc(v, (uint32_t)((n - 1) * (int)a.ldv + NV * 16) * 2);
@@ -770,19 +771,31 @@ __global__ __launch_bounds__(64 * (3 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
           const int e = u * 64 + lane;
           dma16(dst + L::kV + u * 1024, rv, (uint32_t)(e / CV * (int)a.ldv * 2 + e % CV * 16));
         }
+      } else {
+        const uint32_t ff = part == 1 ? 0u : kOffA;
+#pragma unroll
+        for (int u = 0; u < kPart2; ++u)
+          dma16(dst + L::kF + ff + u * 1024, rf, ff + u * 1024 + lane * 16);
       }
     };
     if (chunks > 0) {
       copy(0, 0);
       copy(0, 1);
+      copy(0, 2);
     }
     for (int c = 0; c < chunks; ++c) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kPart2) : "memory");    // all of chunk c but A
       lds_barrier();
-      if (c + 1 < chunks) copy(c + 1, 0);
+      if (c + 1 < chunks) {
+        copy(c + 1, 0);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kPart0) : "memory");  // A
+      } else {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      }
       lds_barrier();
       if (c + 1 < chunks) copy(c + 1, 1);
       lds_barrier();
+      if (c + 1 < chunks) copy(c + 1, 2);
     }
   } else if (wave >= NV) {
     // ---- a state wave: lane (dv, grp) holds dk 32 s + 8 grp + 0 .. 7 of its half's steps s in
@@ -861,6 +874,23 @@ __global__ __launch_bounds__(64 * (3 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
           tl[i] = at(fo + buf + L::kF + (frag_of(2 + i, 1) * 2 + 1) * kFragBytes);
         }
       }
+      // ---- S': what does not need U
+      f16x8 k[HS][2][2];
+#pragma unroll
+      for (int s = 0; s < HS; ++s)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            // rows rho of tile m are dk 32 (m / 2) + 8 (rho / 4) + 4 (m & 1) + rho % 4
+            const uint32_t o = ko[s] + buf + 32 * p * D * 2 + 8 * m;
+            k[s][p][m] = join8(lds_get_tr(o), lds_get_tr(o + 4 * D * 2));
+          }
+      const float gc = lds_get<float>(lds + buf + L::kGate + (kC - 1) * 4);
+#pragma unroll
+      for (int m = 0; m < 2 * HS; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) st[m][r] *= gc;
       lds_barrier();
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -887,25 +917,8 @@ __global__ __launch_bounds__(64 * (3 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
 #pragma unroll
         for (int i = 0; i < 2; ++i) lds_put(uo + (4 + i) * kFragBytes, u[2 + i]);
       }
-      // ---- S': what does not need U meanwhile
-      f16x8 k[HS][2][2];
-#pragma unroll
-      for (int s = 0; s < HS; ++s)
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            // rows rho of tile m are dk 32 (m / 2) + 8 (rho / 4) + 4 (m & 1) + rho % 4
-            const uint32_t o = ko[s] + buf + 32 * p * D * 2 + 8 * m;
-            k[s][p][m] = join8(lds_get_tr(o), lds_get_tr(o + 4 * D * 2));
-          }
 #pragma unroll
       for (int tt = 0; tt < 4; ++tt) d[tt] = lds_get<f32x4>(go + buf + (kC + kTok[tt]) * 4);
-      const float gc = lds_get<float>(lds + buf + L::kGate + (kC - 1) * 4);
-#pragma unroll
-      for (int m = 0; m < 2 * HS; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) st[m][r] *= gc;
       lds_barrier();
       if (hf == 0) {
 #pragma unroll
