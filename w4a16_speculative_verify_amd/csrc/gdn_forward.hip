@@ -36,6 +36,7 @@
 #include "w4v_launch.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace w4v {
 
@@ -281,19 +282,34 @@ __device__ __forceinline__ void put16(float* C, int ldc, const f32x4& v, float s
 __device__ __forceinline__ void gate_products(float al, float (*s_end)[9], float* g, float* d) {
   const int lane = threadIdx.x & 63, own = lane >> 3;
   float up = al, down = 1.f;               // prod over block start .. t, and t + 1 .. block end
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    const float x = __shfl_up(al, i, 64), y = __shfl_down(al, i, 64);
-    if (i <= (lane & 7)) up *= x;
-    if (i <= 7 - (lane & 7)) down *= y;
-  }
+  const auto step = [&](auto i) {          // the gates i lanes below and above, inside rows of 16
+    constexpr int n = decltype(i)::value;
+    const int x = __builtin_bit_cast(int, al);
+    const float lo = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, x, 0x110 + n, 0xf, 0xf, true));
+    const float hi = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, x, 0x100 + n, 0xf, 0xf, true));
+    up *= n <= (lane & 7) ? lo : 1.f;
+    down *= n <= 7 - (lane & 7) ? hi : 1.f;
+  };
+  step(std::integral_constant<int, 1>());
+  step(std::integral_constant<int, 2>());
+  step(std::integral_constant<int, 3>());
+  step(std::integral_constant<int, 4>());
+  step(std::integral_constant<int, 5>());
+  step(std::integral_constant<int, 6>());
+  step(std::integral_constant<int, 7>());
   float v = up;
 #pragma unroll
   for (int k = 6; k >= -1; --k) {          // block k + 1 whole: its last lane's product
-    const float whole = __shfl(up, 8 * (k + 1) + 7, 64);
-    if (k + 1 < own) v *= whole;
+    const float whole = __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, up), 8 * (k + 1) + 7));
+    v *= k + 1 < own ? whole : 1.f;
     if (k >= 0) s_end[lane][k] = k + 1 <= own ? v : 1.f;
-    if (k + 1 > own) down *= whole;
+  }
+#pragma unroll
+  for (int k = 1; k < 8; ++k) {
+    const float whole = __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, up), 8 * k + 7));
+    down *= k > own ? whole : 1.f;
   }
   *g = v;
   *d = down;
@@ -317,16 +333,16 @@ __device__ __forceinline__ void invert16(const float* l, float* t, int ld, int j
   float x[16];
 #pragma unroll
   for (int r = 0; r < 16; ++r) {
-    float y = r == j ? 1.f : 0.f;
+    float y[4] = {r == j ? 1.f : 0.f, 0.f, 0.f, 0.f};      // four chains
 #pragma unroll
     for (int i = 0; i < r; i += 4) {
       const f32x4 v = *reinterpret_cast<const f32x4*>(l + r * ld + i);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (i + e < r) y = __builtin_fmaf(-v[e], x[i + e], y);
+        if (i + e < r) y[e] = __builtin_fmaf(-v[e], x[i + e], y[e]);
     }
-    x[r] = y;
-    t[r * ld + j] = y;
+    x[r] = (y[0] + y[1]) + (y[2] + y[3]);
+    t[r * ld + j] = x[r];
   }
 }
 
