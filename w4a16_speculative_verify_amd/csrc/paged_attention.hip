@@ -503,13 +503,23 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
   };
   // lane j: the page of the wave's keys in tile pages_at + j, so that the table is read once in 64
   // tiles and a tile's page costs no wait
-  int pages = -1, pages_at = t_lo - 64;
+  int pages, pages_at;
+  const auto refill = [&](int t) {
+    pages_at = t;
+    const int tt = t + lane;
+    pages = tt < t_hi ? page_of(tt * L::KT + wave * L::KW) : -1;
+  };
+  // bad: some page of the block's keys lies outside the cache; only then tiles that every row sees are
+  // looked at key by key.  The waves' first pages are those of the first 64 tiles.
+  if (threadIdx.x < 2) s_dirty[threadIdx.x] = 0;
+  refill(t_lo);
+  bool bad = t_lo + lane < t_hi && (t_lo + lane) * L::KT + wave * L::KW < end && pages < 0;
+  for (int k = (t_lo + 64) * L::KT + 16 * (int)threadIdx.x; k < min(t_hi * L::KT, end);
+       k += 16 * 64 * NW)
+    bad |= page_of(k) < 0;
+  bad = __syncthreads_or(bad);
   const auto issue = [&](int t, int slot) {
-    if (t - pages_at >= 64) {
-      pages_at = t;
-      const int tt = t + lane;
-      pages = tt < t_hi ? page_of(tt * L::KT + wave * L::KW) : -1;
-    }
+    if (t - pages_at >= 64) refill(t);
     const int key = t * L::KT + wave * L::KW;
     const int pg = __builtin_amdgcn_readlane(pages, t - pages_at);
     const int64_t off =
@@ -523,14 +533,6 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
       dma16(dst + L::kHalf + u * 1024, rv, vo[u]);
     }
   };
-  // whether any page of the block's keys lies outside the cache: only then tiles that every row
-  // sees are looked at key by key
-  if (threadIdx.x < 2) s_dirty[threadIdx.x] = 0;
-  bool bad = false;
-  for (int k = t_lo * L::KT + 16 * (int)threadIdx.x; k < min(t_hi * L::KT, end);
-       k += 16 * 64 * NW)
-    bad |= page_of(k) < 0;
-  bad = __syncthreads_or(bad);
 #pragma unroll
   for (int s = 0; s + 1 < L::NS; ++s) issue(t_lo + s, s);
 
