@@ -796,12 +796,16 @@ AttnPlan plan_attention(int B, int max_q, int max_ctx, int Hq, int Hkv, int D) {
   p.row_tiles = (int)((rows + p.rows - 1) / p.rows);
   const int64_t items = (int64_t)B * Hkv * p.row_tiles;
   const int tiles = (max_ctx + 31) / 32;
-  // Blocks that the CUs hold at a time: while there are fewer row tiles, contexts are split, down to 8
-  // tiles of 32 keys a block.  (One token a sequence, 8 key heads, us at 256 / 512 / 1,024 blocks: 4
-  // sequences of 8,192 tokens 27 / 32 / 48, 16 of 16,384 188 / 190 / 196; splits of 16 or 32 tiles and
-  // more: 1 of 1,001 tokens 11 and 13.5 against 8.9, 1 of 8,208 14 and 18 against 13.)
+  // While there are fewer row tiles than the CUs hold blocks, contexts are split: down to 8 tiles of 32
+  // keys a block, and while every block has a CU of its own down to 4 (2 for more than 32 rows, whose
+  // blocks have two waves).  us, one token a sequence, 8 key heads: 4 sequences of 8,192 tokens on 256 /
+  // 512 / 1,024 blocks 27 / 32 / 48; 1 of 1,001 in splits of 2 / 4 / 8 / 16 tiles 8.7 / 8.0 / 9.2 / 11.
+  // 16 tokens a sequence: 8 of 8,213 on 256 / 512 / 1,024 blocks 67 / 49 / 59; 1 of 1,016 in splits of
+  // 1 / 2 / 4 / 8 / 16 tiles 10.9 / 10.4 / 11.7 / 14.9 / 21.
   const int blocks = p.rows <= 32 || (p.rows == 256 && D == 128) ? 256 : 512;
   int64_t splits = items < blocks ? std::min<int64_t>(blocks / items, tiles / 8) : 1;
+  if (items < 256)
+    splits = std::max(splits, std::min<int64_t>(256 / items, tiles / (p.rows <= 32 ? 4 : 2)));
   // Many long sequences, seldom of one length: splits of 128 tiles and more, up to 2,048 blocks, even
   // out what the CUs get (64 ragged sequences up to 16,384 tokens 527 -> 480 us; shorter splits cost
   // more than they give, 64 of 2,048 tokens 98 unsplit, 110 in two).
