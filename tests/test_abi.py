@@ -365,7 +365,7 @@ def rope(lib, qkv=G, ldqkv=6144, q=2 * G, ldq=4096, kc=3 * G, vc=5 * G, pages=10
     (dict(N=-1), INVALID), (dict(B=-1), INVALID), (dict(Hq=30), INVALID), (dict(Hkv=0), INVALID),
     (dict(pages=0), INVALID), (dict(max_pages=0), INVALID), (dict(page=0), INVALID),
     (dict(D=96), UNSUPPORTED), (dict(page=48), UNSUPPORTED), (dict(page=8), UNSUPPORTED),
-    (dict(page=2048), UNSUPPORTED), (dict(B=65536), UNSUPPORTED), (dict(rot=24), UNSUPPORTED),
+    (dict(page=2048), UNSUPPORTED), (dict(B=65536), UNSUPPORTED), (dict(max_pages=(1 << 24) + 1), UNSUPPORTED), (dict(rot=24), UNSUPPORTED),
     (dict(rot=144), INVALID), (dict(rot=-16), INVALID), (dict(inv=None), INVALID),
     (dict(qkv=None), INVALID), (dict(q=None), INVALID), (dict(kc=None), INVALID),
     (dict(table=None), INVALID), (dict(cu=None), INVALID), (dict(ctx=None), INVALID),
@@ -462,7 +462,8 @@ def gdn(lib, q=G, ldq=2048, k=2 * G, ldk=2048, v=3 * G, ldv=2048, al=4 * G, be=5
     (dict(B=0), OK), (dict(N=0, so=None), OK), (dict(N=0, so=6 * G), OK),
     (dict(N=-1), INVALID), (dict(B=-1), INVALID), (dict(max_t=-1), INVALID), (dict(Hk=0), INVALID),
     (dict(Hk=3), INVALID), (dict(D=96), UNSUPPORTED), (dict(D=256), UNSUPPORTED),
-    (dict(B=70000), UNSUPPORTED), (dict(Hk=1, H=70000, ldv=70000 * 128), UNSUPPORTED),
+    (dict(B=70000), UNSUPPORTED), (dict(B=60000, H=1600, ldv=1600 * 128, ldo=1600 * 128), UNSUPPORTED),
+    (dict(ldk=1 << 23), UNSUPPORTED), (dict(Hk=1, H=70000, ldv=70000 * 128), UNSUPPORTED),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(al=None), INVALID),
     (dict(be=None), INVALID), (dict(cu=None), INVALID), (dict(s=None), INVALID), (dict(o=None), INVALID),

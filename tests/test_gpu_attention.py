@@ -364,6 +364,66 @@ def test_captured_calls_follow_the_lengths(lib):
         assert torch.equal(got, o2), lens
 
 
+@pytest.mark.parametrize("new", [1, 9, 16, 60])
+@pytest.mark.parametrize("max_ctx", [0, 1, 40, 1 << 20])
+def test_the_context_hint_shapes_the_launch_only(lib, new, max_ctx):
+    rng = np.random.default_rng(new)
+    x = gen.paged_batch(rng, [new, new], [1500, 300], 4, 1, 128, 64)
+    run_attention(lib, x, max_ctx=max_ctx)
+
+
+def test_rows_past_max_q_are_left(lib):
+    import torch
+    rng = np.random.default_rng(16)
+    x = gen.paged_batch(rng, [12, 30], [100, 90], 4, 2, 64, 16)
+    args = [dev(a) for a in (x.q, x.k_cache, x.v_cache, x.table, x.cu, x.ctx)]
+    want = host(lib.paged_attention(*args, 30))
+    out = torch.full(x.q.shape, 7.0, dtype=torch.float16, device="cuda")
+    lib.paged_attention(*args, 12, out=out)
+    torch.cuda.synchronize()
+    got = host(out)
+    assert np.allclose(got[:24].astype(np.float64), want[:24].astype(np.float64), rtol=2e-3, atol=2e-3)
+    assert np.all(got[24:] == 7.0)
+
+
+def test_two_streams_at_once(lib):
+    """Calls that overlap in time on two streams, each with its own workspace."""
+    import torch
+    rng = np.random.default_rng(17)
+    x = gen.paged_batch(rng, [4, 16], [2500, 3000], 8, 2, 128, 32)
+    args = [dev(a) for a in (x.q, x.k_cache, x.v_cache, x.table, x.cu, x.ctx)]
+    want = lib.paged_attention(*args, 16)
+    one = lib.paged_attention(args[0][:4].contiguous(), *args[1:3], args[3][:1].contiguous(),
+                              args[4][:2].contiguous(), args[5][:1].contiguous(), 4)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        got[0].append(lib.paged_attention(*args, 16, stream=streams[0]))
+        got[1].append(lib.paged_attention(args[0][:4], *args[1:3], args[3][:1].contiguous(), args[4][:2],
+                                          args[5][:1], 4, stream=streams[1]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got[0]) and all(torch.equal(g, one) for g in got[1])
+
+
+def test_one_workspace_for_different_calls(lib):
+    """Calls of other shapes and kinds on one stream share a workspace whose counters they leave at
+    zero."""
+    import torch
+    rng = np.random.default_rng(18)
+    ws = lib.new_workspace(64 << 20)
+    for new, ctx in ((1, 3000), (16, 5000), (8, 900), (40, 2000), (1, 3000)):
+        x = gen.paged_batch(rng, [new], [ctx], 8, 2, 64, 16)
+        run_attention(lib, x, workspace=ws)
+        h = torch.randn((96, 2, 64), device="cuda").half()
+        h = h / h.float().norm(dim=-1, keepdim=True).half()
+        g = torch.rand((96, 2), device="cuda")
+        s = torch.zeros((1, 2, 64, 64), device="cuda")
+        lib.gdn_forward(h, h, h, g, g, torch.tensor([0, 96], dtype=torch.int32, device="cuda"), s, 96,
+                        state_out=s, workspace=ws)
+        assert int(ws[:64 * 1024].to(torch.int32).sum()) == 0
+
+
 def test_repeats_are_bit_identical(lib):
     import torch
     rng = np.random.default_rng(15)

@@ -547,13 +547,19 @@ def _paged(k_cache, v_cache, block_table, cu, ctx_lens, device):
     return (*shape, b)
 
 
+TICKET_BYTES = 64 * 1024     # a workspace's arrival counters
+
+
 def _scratch(workspace, need, device):
     """(pointer, bytes, the tensor that holds it) of a call's workspace, allocated where none is given."""
     if workspace is None:
         if need == 0:
             return None, 0, None
-        workspace = new_workspace(need, device)
-        return workspace.data_ptr(), need, workspace
+        import torch
+        workspace = torch.empty(need + 256, dtype=torch.uint8, device=device)
+        off = -workspace.data_ptr() % 256
+        workspace[off:off + min(need, TICKET_BYTES)].zero_()      # the counters; the rest is scratch
+        return workspace.data_ptr() + off, need, workspace
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace

@@ -596,7 +596,7 @@ int paged_sizes(int N, int B, int Hq, int Hkv, int D, int num_pages, int page_si
       max_pages < 1 || Hq % Hkv != 0)
     return W4V_ERR_INVALID_ARG;
   if ((D != 64 && D != 128 && D != 256) || page_size < 16 || page_size > 1024 ||
-      (page_size & (page_size - 1)) != 0 || B > kMaxGridYZ || max_pages > INT32_MAX ||
+      (page_size & (page_size - 1)) != 0 || B > kMaxGridYZ || max_pages > (1 << 30) / page_size ||
       (int64_t)(Hq + 2ll * Hkv) * D > INT32_MAX)
     return W4V_ERR_UNSUPPORTED;
   return W4V_OK;
@@ -715,7 +715,8 @@ namespace {
 int gdn_sizes(int N, int B, int max_t, int Hk, int H, int D) {
   if (N < 0 || B < 0 || max_t < 0 || Hk < 1 || H < 1 || D < 1 || H % Hk != 0)
     return W4V_ERR_INVALID_ARG;
-  if ((D != 64 && D != 128) || B > kMaxGridYZ || H > kMaxGridYZ) return W4V_ERR_UNSUPPORTED;
+  if ((D != 64 && D != 128) || B > kMaxGridYZ || H > kMaxGridYZ || (int64_t)B * H > (1 << 24))
+    return W4V_ERR_UNSUPPORTED;
   return W4V_OK;
 }
 
