@@ -1,4 +1,46 @@
-// Attention of a chunk of new tokens over a paged key/value cache, gfx950.
+// Attention of a chunk of new tokens over a paged key/value cache, gfx950 ("Efficient LLM Challenge
+// Results", section 3: the target's forward pass over the K + 1 positions of the verify block, and over
+// its prompts).
+//
+//   o = sum_p w_p v_p,  w = softmax_p(scale q . k_p) over the positions p <= the row's own
+//
+// The G query heads of a key/value head and the chunk's tokens are packed into rows that share that
+// head's keys: row x is token x / G, head x % G.  One pass over the keys with a running maximum m and
+// sum l (fp32, base 2): S^T = K Q^T on the matrix cores, so that a lane holds one row's scores for
+// several keys; P^T = 2^(c S^T - m); O^T += V^T P^T, scaled by 2^(m - m') when the maximum moves.  The
+// maximum moves only when a score passes it by 2^8 (weights stay below 256, exact enough in fp16), so
+// the 2^(m - m') pass over O^T is rare.  The scores' registers are the next product's operand as they
+// are: a lane that holds keys 4 g .. 4 g + 3 of a row in S^T gives them as its part of the k index, and
+// V^T is read from LDS by the transposing read in the same order.  Weights are rounded to fp16 for that
+// product (their rounding errors are independent over the keys, about as much as the result's own
+// rounding once); with few rows, where the matrix cores idle, they are given as pairs of fp16 (hi +
+// remainder), which cost 0 to 5 %.
+//
+// Copies: a page's keys of one head are contiguous, so keys and values go global -> LDS by DMA (1 KiB
+// an instruction, no registers), from a resource that ends with the sequence or has no bytes where a
+// table entry points outside the cache: what is not there arrives as zeros.  A lane copies the chunk
+// that the swizzle of its LDS place asks for: chunk (16 bytes) c of key r sits at c ^ f(r), with f such
+// that neither the operand reads of K (16 rows, one chunk) nor the transposing reads of V (rows of 4 or
+// 8 keys, neighbouring chunks) meet a bank twice (0 conflict cycles counted).
+//
+// Few rows (<= 32; attn_stream_kernel): bound by the cache's bytes.  The four waves of a block take
+// every fourth tile of 32 keys (16 at D = 256) for all rows, each with a ring of its own and no barrier,
+// and join their sums in LDS at the end.
+//   64 sequences up to 16,384 tokens, 8 key heads of 128: 484 us, 5.8 TB/s (a copy of 2 GiB reaches 4.9
+//   on this card, a plain read 6.0); a table entry read by a scalar load per 16 keys, its wait before
+//   every copy, took 628.
+// More rows (attn_tile_kernel): 2, 4 or 8 waves of 32 rows share tiles of 64 keys (32 with two waves, or
+// at D = 256), on the 32 x 32 instruction, one barrier a tile.  Verify blocks are bound by the bytes
+// again (8 x 21 rows over 8,213 tokens 49 us, 4.2 TB/s), prompts by the matrix cores and the conversions
+// beside them: 8,192 tokens 32 / 8 heads of 128 575 us, 956 TFLOP/s, where a loop of nothing but these
+// matrix instructions reaches 1,330-1,550 on this card (the clock falls to 2.0 GHz) and one with seven
+// vector instructions a product, about this kernel's mix, 1,120-1,190.  Scores of the next tile
+// computed beside this one's weights, values read ahead, two blocks of four waves a CU and other wave
+// priorities took 7-12 %, 4 %, 3 % and 0 % longer than this form, timed in turn.
+//
+// Contexts are split over blocks where rows are few (plan_attention); partial sums (fp32, with m and l)
+// are joined in the splits' order, by the row tile's last block when they are few, else by
+// attn_join_kernel: the result does not depend on the order of arrival.
 #include "w4v_device.h"
 #include "w4v_launch.h"
 
@@ -26,7 +68,7 @@ struct Ring {
   static constexpr int kPer = 2 * NG * kDma;             // and per tile
 };
 
-// Chunk (16 bytes) swizzles inside a group's rows, see the layout notes above.
+// chunk swizzles f of the keys and values of a 16-key group
 template <int D>
 __device__ __forceinline__ int swz_k(int r) {
   return D == 64 ? (r >> 1) & 7 : r & 15;

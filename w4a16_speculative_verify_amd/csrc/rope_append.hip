@@ -14,7 +14,9 @@
 // p = 1e6 the 32-bit product p f_j alone would be off by 0.03 rad.  The table
 // f_j is the caller's, so every scaling for long contexts is one table.
 //
-// Bound by the bytes of qkv, read once and written once.  One block per row:
+// Bound by the bytes of qkv, read once and written once: 8,192 rows of 32 + 2 x 8 heads of 128 in 45 us,
+// 4.4 TB/s (a copy of 2 GiB reaches 4.9 on this card); 128 rows 3.7 us, the launch and three loads one
+// after the other.  One block per row:
 // the rot/2 angles are computed once per row, by one thread each, and shared by
 // all heads through LDS; each thread then moves 32-byte items (two 16-byte
 // chunks that hold 8 whole pairs), whose loads are issued before the angles are
