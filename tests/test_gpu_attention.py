@@ -161,6 +161,20 @@ def test_pages_outside_the_cache_are_not_seen(lib):
     run_attention(lib, x)
 
 
+@pytest.mark.parametrize("new", [1, 14, 40, 90])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_table_that_ends_inside_a_tile(lib, new, d):
+    """Positions past the table, with every entry of it good: the last page ends inside a tile whose
+    other keys every row would see if they were there."""
+    rng = np.random.default_rng(new + d)
+    x = gen.paged_batch(rng, [new, 1], [80, 37], 4, 1, d, 16)     # 5 pages: 64 + 16 and 2 x 32 + 16
+    x.ctx[0] = 80 + 70 + new
+    run_attention(lib, x)
+    x = gen.paged_batch(rng, [new], [48], 4, 1, d, 16)
+    x.ctx[0] = 2000
+    run_attention(lib, x)
+
+
 @pytest.mark.parametrize("order", ["rising", "falling", "wide"])
 def test_moving_maxima(lib, order):
     """Scores that rise by hundreds along the context (the running maximum moves at nearly every

@@ -175,7 +175,7 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
   const int nt = (end + L::KT - 1) / L::KT;
   const int t_lo = (int)((int64_t)nt * split / splits);
   const int t_hi = (int)((int64_t)nt * (split + 1) / splits);
-  const int all_see = sq.p0 + row0 / G;                        // keys up to here every row sees
+  const int all_see = min(sq.p0 + row0 / G, sq.len - 1);       // keys up to here every row sees
 
   // DMA source offsets of this lane inside a group: LDS chunk position -> chunk
   uint32_t ko[L::kDma], vo[L::kDma];
@@ -607,7 +607,7 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
   int slot = 0;
   // tiles up to clear every row of the block sees whole; the others (the last one or two of a causal
   // context) pay for the masks
-  const int clear = bad ? t_lo : (sq.p0 + row0 / G + 1) / L::KT;
+  const int clear = bad ? t_lo : min(sq.p0 + row0 / G + 1, sq.len) / L::KT;
   for (int t = t_lo; t < t_hi; ++t) {
     // tile t has landed, and every wave is done with tile t - 1, whose place the next copy takes
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"((L::NS - 2) * 2 * L::kDma) : "memory");
