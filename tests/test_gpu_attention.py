@@ -146,6 +146,23 @@ def test_later_positions_may_hold_anything(lib, new, d):
     assert np.all(np.isfinite(got[new:]))
 
 
+@pytest.mark.parametrize("new", [1, 4, 9, 40])
+def test_nan_queries_and_keys_reach_their_rows(lib, new):
+    """A query of NaN, and a stretch of keys of NaN that fills whole splits, show in the rows that they
+    belong to, whichever blocks share the context, and nowhere else."""
+    rng = np.random.default_rng(new)
+    x = gen.paged_batch(rng, [new, new], [5000, 4100], 4, 2, 64, 16)
+    clean, _ = run_attention(lib, x)
+    x.q[0, 1] = np.nan
+    for p in range(0, 4000):
+        x.k_cache[x.table[1, p // 16], 0, p % 16] = np.nan     # key head 0: query heads 0 and 1
+    args = [dev(a) for a in (x.q, x.k_cache, x.v_cache, x.table, x.cu, x.ctx)]
+    got = host(lib.paged_attention(*args, new, 5000))
+    nan = np.zeros(got.shape[:2], bool)
+    nan[0, 1] = nan[new:, :2] = True
+    assert np.all(np.isnan(got[nan])) and np.array_equal(got[~nan], clean[~nan])
+
+
 def test_pages_outside_the_cache_are_not_seen(lib):
     """Entries inside the context that point nowhere, and a context longer than its table."""
     rng = np.random.default_rng(5)

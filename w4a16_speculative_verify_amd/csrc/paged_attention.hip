@@ -450,14 +450,15 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const uint32_t mk = ml[k][0], lk = ml[k][1];
-        const float m1 = s0 + k < splits ? __builtin_bit_cast(float, mk) : -INFINITY;
-        const float l1 = __builtin_bit_cast(float, lk);
+        if (s0 + k >= splits) break;
+        // a split without keys to see has zeros, one whose scores are all NaN has NaN in l1 and v
+        const float m1 = __builtin_bit_cast(float, mk), l1 = __builtin_bit_cast(float, lk);
         const float mn = fmaxf(mx, m1), mu = mn == -INFINITY ? 0.f : mn;
         const float f = __builtin_amdgcn_exp2f(mx - mu);
         const float g = __builtin_amdgcn_exp2f(m1 - mu);
-        sum = sum * f + (m1 == -INFINITY ? 0.f : g * l1);
+        sum = sum * f + g * l1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = acc[e] * f + (m1 == -INFINITY ? 0.f : g * v[k][e]);
+        for (int e = 0; e < 4; ++e) acc[e] = acc[e] * f + g * v[k][e];
         mx = mn;
       }
     }
