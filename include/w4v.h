@@ -311,7 +311,8 @@ int gdn_state_commit(float* state, const float* k, const float* v, const float* 
  * state    fp32 [B x H x D x D] (S[b, h] is [dv x dk] row-major), 16-byte aligned;
  *          state_out the same, equal to state (in place), disjoint from it, or NULL.
  *          o and state_out overlap no input (o not q, k, v; state aside).
- * Sizes    D 64 or 128; B, H <= 65535, B * H <= 2^24; row strides of q, k, v below 2^23
+ * Sizes    D 64 or 128; B, H <= 65535, B * H * D <= 2^28; row strides of q, k, v
+ *          below 2^23
  *          (W4V_ERR_UNSUPPORTED otherwise).
  * max_t    the most rows a sequence has: chooses the form (the results stay right
  *          whatever it is).  fp16 inputs with max_t above 16 go 32 positions at a
@@ -354,9 +355,9 @@ int gdn_forward(const void* q, int64_t ldq, const void* k, int64_t ldk, const vo
  *            not stored, and no row sees it.  Pages may be shared by sequences for
  *            reading; two rows written to one slot race.
  * Sizes      D 64, 128 or 256; page_size a power of two, 16 .. 1024; max_pages *
- *            page_size <= 2^30; B <= 65535 (W4V_ERR_UNSUPPORTED otherwise); Hq a
- *            multiple of Hkv (query head j reads key/value head j / (Hq / Hkv)).
- *            B == 0 or N == 0: nothing to do.
+ *            page_size <= 2^30; B <= 65535; N < 2^24 (W4V_ERR_UNSUPPORTED
+ *            otherwise); Hq a multiple of Hkv (query head j reads key/value head
+ *            j / (Hq / Hkv)).  B == 0 or N == 0: nothing to do.
  * All pointers are device pointers; int32 and fp32 ones are 4-byte aligned.
  * ---------------------------------------------------------------------- */
 

@@ -365,7 +365,8 @@ def rope(lib, qkv=G, ldqkv=6144, q=2 * G, ldq=4096, kc=3 * G, vc=5 * G, pages=10
     (dict(N=-1), INVALID), (dict(B=-1), INVALID), (dict(Hq=30), INVALID), (dict(Hkv=0), INVALID),
     (dict(pages=0), INVALID), (dict(max_pages=0), INVALID), (dict(page=0), INVALID),
     (dict(D=96), UNSUPPORTED), (dict(page=48), UNSUPPORTED), (dict(page=8), UNSUPPORTED),
-    (dict(page=2048), UNSUPPORTED), (dict(B=65536), UNSUPPORTED), (dict(max_pages=(1 << 24) + 1), UNSUPPORTED), (dict(rot=24), UNSUPPORTED),
+    (dict(page=2048), UNSUPPORTED), (dict(B=65536), UNSUPPORTED), (dict(N=1 << 24), UNSUPPORTED),
+    (dict(max_pages=(1 << 24) + 1), UNSUPPORTED), (dict(rot=24), UNSUPPORTED),
     (dict(rot=144), INVALID), (dict(rot=-16), INVALID), (dict(inv=None), INVALID),
     (dict(qkv=None), INVALID), (dict(q=None), INVALID), (dict(kc=None), INVALID),
     (dict(table=None), INVALID), (dict(cu=None), INVALID), (dict(ctx=None), INVALID),
@@ -383,6 +384,12 @@ def test_rope_kv_append_validation(lib, kw, status):
     assert rope(lib, **kw) == status
 
 
+def test_workspace_size_of_more_rows_than_a_call_takes(lib):
+    for hq in (1, 32, 1 << 10, 1 << 20):
+        assert lib.paged_attention_workspace_size(1, 2**31 - 1, 100, hq, 1, 64) == 0 or hq == 1
+        assert lib.paged_attention_workspace_size(1, 1 << 30, 1 << 30, hq, 1, 64) == 0
+
+
 def attn(lib, q=G, ldq=4096, kc=3 * G, vc=5 * G, pages=100, page=64, table=A, max_pages=32, cu=A,
          ctx=A, out=2 * G, ldo=4096, N=16, B=1, max_q=16, max_ctx=100, Hq=32, Hkv=8, D=128, scale=0.1,
          ws=A, wsb=1 << 30):
@@ -396,6 +403,7 @@ def attn(lib, q=G, ldq=4096, kc=3 * G, vc=5 * G, pages=100, page=64, table=A, ma
     (dict(Hq=33), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(D=80), UNSUPPORTED), (dict(page=24), UNSUPPORTED), (dict(B=1 << 20), UNSUPPORTED),
+    (dict(N=1 << 24), UNSUPPORTED), (dict(max_q=1 << 27), UNSUPPORTED),
     (dict(max_q=1 << 30, N=1 << 30), UNSUPPORTED),
     (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(kc=None), INVALID),
     (dict(vc=None), INVALID), (dict(cu=None), INVALID), (dict(table=None), INVALID),

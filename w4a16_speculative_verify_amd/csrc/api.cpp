@@ -597,6 +597,7 @@ int paged_sizes(int N, int B, int Hq, int Hkv, int D, int num_pages, int page_si
     return W4V_ERR_INVALID_ARG;
   if ((D != 64 && D != 128 && D != 256) || page_size < 16 || page_size > 1024 ||
       (page_size & (page_size - 1)) != 0 || B > kMaxGridYZ || max_pages > (1 << 30) / page_size ||
+      N >= (1 << 24) ||                    // a block of 256 threads a row, below 2^32 threads
       (int64_t)(Hq + 2ll * Hkv) * D > INT32_MAX)
     return W4V_ERR_UNSUPPORTED;
   return W4V_OK;
@@ -658,7 +659,7 @@ int rope_kv_append(const void* qkv, int64_t ldqkv, void* q_out, int64_t ldq, voi
 }
 
 size_t paged_attention_workspace_size(int B, int max_q, int max_ctx, int Hq, int Hkv, int D) {
-  if (B <= 0 || max_q <= 0 || max_ctx < 0 ||
+  if (B <= 0 || max_q <= 0 || max_ctx < 0 || (int64_t)max_q * Hq > INT32_MAX ||
       paged_sizes(1, B, Hq, Hkv, D, 1, 16, 1) != W4V_OK)
     return 0;
   return w4v::plan_attention(B, max_q, max_ctx, Hq, Hkv, D).workspace;
@@ -715,7 +716,8 @@ namespace {
 int gdn_sizes(int N, int B, int max_t, int Hk, int H, int D) {
   if (N < 0 || B < 0 || max_t < 0 || Hk < 1 || H < 1 || D < 1 || H % Hk != 0)
     return W4V_ERR_INVALID_ARG;
-  if ((D != 64 && D != 128) || B > kMaxGridYZ || H > kMaxGridYZ || (int64_t)B * H > (1 << 24))
+  // (the scan's B H D / 32 blocks of 448 threads stay below 2^32 threads)
+  if ((D != 64 && D != 128) || B > kMaxGridYZ || H > kMaxGridYZ || (int64_t)B * H * D > (1 << 28))
     return W4V_ERR_UNSUPPORTED;
   return W4V_OK;
 }
