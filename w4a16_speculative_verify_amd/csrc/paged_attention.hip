@@ -29,8 +29,11 @@
 //   64 sequences up to 16,384 tokens, 8 key heads of 128: 484 us, 5.8 TB/s (a copy of 2 GiB reaches 4.9
 //   on this card, a plain read 6.0); a table entry read by a scalar load per 16 keys, its wait before
 //   every copy, took 628.
-// More rows (attn_tile_kernel): 2, 4 or 8 waves of 32 rows share tiles of 64 keys (32 with two waves, or
-// at D = 256), on the 32 x 32 instruction, one barrier a tile.  Verify blocks are bound by the bytes
+// More rows (attn_tile_kernel): 2, 4 or 8 waves of 32 rows share tiles of 64 keys (32 at D = 256), on
+// the 32 x 32 instruction, one barrier a tile.  64 rows take four waves, two for either half of a
+// tile's keys, joined in LDS: with two waves alone the CU waits for the chain of one (32 sequences x
+// 8 tokens over 8,208, D = 64, 80 -> 54 us; 64 x 16 over 8,208, D = 128, 376 -> 365; 128 rows lose,
+// 411 -> 476, and D = 256 has the registers for one wave a SIMD, 61 -> 80).  Verify blocks are bound by the bytes
 // again (8 x 21 rows over 8,213 tokens 49 us, 4.2 TB/s), prompts by the matrix cores and the conversions
 // beside them: 8,192 tokens 32 / 8 heads of 128 575 us, 956 TFLOP/s, where a loop of nothing but these
 // matrix instructions reaches 1,330-1,550 on this card (the clock falls to 2.0 GHz) and one with seven
@@ -472,21 +475,24 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
 }
 
 // ------------------------------------------------------------------ many rows
-// NW waves of 32 packed rows, keys per tile and tiles in the ring; a wave copies KT / NW keys of a
-// tile, at most 16, which lie in one page
-template <int D, int NW>
+// NW waves, in KS groups: the waves of a group take 32 packed rows each, the groups every KS-th 32 keys
+// of a tile; keys per tile and tiles in the ring.  A wave copies KT / NW keys of a tile, at most 16,
+// which lie in one page.
+template <int D, int NW, int KS>
 struct TileRing {
-  static constexpr int kRows = 32 * NW;
-  static constexpr int KT = D == 256 || NW == 2 ? 32 : 64;
-  static constexpr int NSub = KT / 32;                   // 32-key steps of a tile
-  static constexpr int NG = KT / 16;                     // 16-key groups (pages end on them)
+  static constexpr int kRowWaves = NW / KS;
+  static constexpr int kRows = 32 * kRowWaves;
+  static constexpr int KT = D == 256 ? 32 : 64;
+  static constexpr int NSub = KT / 32 / KS;              // 32-key steps of a wave in a tile
+  static constexpr int NG = KT / 16;                     // 16-key groups of a tile (pages end on them)
   static constexpr uint32_t kHalf = KT * D * 2;          // bytes of a tile's keys (or values)
-  static constexpr int NS = 2 * kHalf == 32768 ? 2 : 2 * kHalf == 16384 ? 4 : 6;
+  static constexpr uint32_t kTile = 2 * kHalf;
+  static constexpr int NS = kTile == 16384 ? 4 : 2;
   static constexpr int KW = KT / NW;
   static constexpr int kDma = KW * D * 2 / 1024;         // DMA instructions per wave and half
   // blocks of a CU (registers: D = 256 takes a SIMD's 512 for one wave)
-  static constexpr int kPerCU = NW == 8 ? (D == 64 ? 2 : 1) : 2;
-  static constexpr int kPerSimd = D == 256 ? 1 : NW == 8 ? 2 * kPerCU : 2;
+  static constexpr int kPerCU = NW == 8 && D == 128 ? 1 : 2;
+  static constexpr int kPerSimd = D == 256 ? 1 : NW * kPerCU / 4;
 };
 template <int D>
 __device__ __forceinline__ int tswz_k(int r) {
@@ -501,15 +507,17 @@ __device__ __forceinline__ f32x16 mfma32x32x16(const f16x8& a, const f16x8& b, c
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-template <int D, int NW>
-__global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_tile_kernel(
+template <int D, int NW, int KS>
+__global__ __launch_bounds__(64 * NW, (TileRing<D, NW, KS>::kPerSimd)) void attn_tile_kernel(
     AttnArgs a, int splits, float* __restrict__ part) {
-  using L = TileRing<D, NW>;
+  using L = TileRing<D, NW, KS>;
   constexpr int DT = D / 32, DS = D / 16, NSub = L::NSub, kTileRows = L::kRows;
-  __shared__ __attribute__((aligned(1024))) unsigned char s_ring[L::NS * 2 * L::kHalf];
+  __shared__ __attribute__((aligned(1024))) unsigned char s_ring[L::NS * L::kTile];
   __shared__ unsigned long long s_dirty[2];            // keys of a tile with values that are not finite
+  __shared__ float s_ml[L::kRowWaves][2][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row_wave = wave % L::kRowWaves, key_wave = wave / L::kRowWaves;
   const int col = lane & 31, half = lane >> 5;
   const int G = a.Hq / a.Hkv;
   const int h = blockIdx.x % a.Hkv, split = blockIdx.x / a.Hkv;
@@ -524,7 +532,7 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
   const int t_hi = (int)((int64_t)nt * (split + 1) / splits);
 
   // the wave's rows: behind any_see none sees a key
-  const int wr0 = row0 + 32 * wave;
+  const int wr0 = row0 + 32 * row_wave;
   const int x = min(wr0 + col, nrows - 1), xi = x / G, xg = x % G;
   const int lim = min(sq.p0 + xi, sq.len - 1);
   const int any_see = wr0 < nrows ? sq.p0 + min(wr0 + 31, nrows - 1) / G : -1;
@@ -569,7 +577,7 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
         pg < 0 ? 0 : (((int64_t)pg * a.Hkv + h) * a.page_size + (key & (a.page_size - 1))) * D;
     const uint32_t bytes = pg < 0 ? 0u : (uint32_t)min(L::KW, end - key) * (D * 2);
     const u32x4s rk = dma_rsrc(a.k_cache + off, bytes), rv = dma_rsrc(a.v_cache + off, bytes);
-    const uint32_t dst = ring + slot * 2 * L::kHalf + wave * (L::KW * D * 2);
+    const uint32_t dst = ring + slot * L::kTile + wave * (L::KW * D * 2);
 #pragma unroll
     for (int u = 0; u < L::kDma; ++u) {
       dma16(dst + u * 1024, rk, ko[u]);
@@ -596,13 +604,15 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
 
   // lane offsets of the operand reads: keys col of a 32-key step, chunks 2 s + half; values for the
   // transposing reads, keys 4 half + i / 4 of a 16-key step, 16 d of half a row tile
+  const int own = key_wave * NSub * 32;    // the wave's first key in a tile
   uint32_t ka[DS], va[DT];
 #pragma unroll
-  for (int s = 0; s < DS; ++s) ka[s] = ring + col * D * 2 + ((2 * s + half) ^ tswz_k<D>(col)) * 16;
+  for (int s = 0; s < DS; ++s)
+    ka[s] = ring + own * D * 2 + col * D * 2 + ((2 * s + half) ^ tswz_k<D>(col)) * 16;
   const int i16 = lane & 15, vkey = 4 * half + (i16 >> 2);
 #pragma unroll
   for (int d = 0; d < DT; ++d)
-    va[d] = ring + L::kHalf + vkey * D * 2 + (i16 & 1) * 8 +
+    va[d] = ring + L::kHalf + (own + vkey) * D * 2 + (i16 & 1) * 8 +
             ((4 * d + 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1)) ^ tswz_v<D>(vkey)) * 16;
 
   int slot = 0;
@@ -614,7 +624,7 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"((L::NS - 2) * 2 * L::kDma) : "memory");
     lds_barrier();
     issue(t + L::NS - 1, slot == 0 ? L::NS - 1 : slot - 1);
-    const uint32_t so = slot * 2 * L::kHalf;
+    const uint32_t so = slot * L::kTile;
     slot = slot + 1 == L::NS ? 0 : slot + 1;
     const int key0 = t * L::KT;
     const bool hide = t >= clear;
@@ -628,7 +638,7 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
       }
       lds_barrier();
     }
-    if (key0 > any_see) continue;          // none of the wave's rows sees the tile
+    if (key0 + own > any_see) continue;    // none of the wave's rows sees its keys
 
     f32x16 sc[NSub];
 #pragma unroll
@@ -641,19 +651,19 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
         sc[j] = mfma32x32x16(k, q[s], sc[j]);
       }
     }
-    uint32_t ok = (1u << L::NG) - 1;
+    uint32_t ok = (1u << (2 * NSub)) - 1;
     if (hide) {
       if (bad) {
         ok = 0;
 #pragma unroll
-        for (int g = 0; g < L::NG; ++g) ok |= (uint32_t)(page_of(key0 + 16 * g) >= 0) << g;
+        for (int g = 0; g < 2 * NSub; ++g) ok |= (uint32_t)(page_of(key0 + own + 16 * g) >= 0) << g;
       }
 #pragma unroll
       for (int j = 0; j < NSub; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int kk = 32 * j + 8 * (r / 4) + 4 * half + r % 4;
-          const bool see = key0 + kk <= lim && ((ok >> (2 * j + r / 8)) & 1);
+          const bool see = key0 + own + kk <= lim && ((ok >> (2 * j + r / 8)) & 1);
           sc[j][r] = see ? sc[j][r] : -INFINITY;
         }
     }
@@ -695,8 +705,9 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
         }
     }
     if (hide) {
-      for (uint64_t left = s_dirty[t & 1]; left != 0; left &= left - 1) {
-        const int key = key0 + (int)__builtin_ctzll(left), pg = page_of(key);
+      constexpr uint64_t kOwn = NSub == 2 ? ~0ull : 0xffffffffull;
+      for (uint64_t left = (s_dirty[t & 1] >> own) & kOwn; left != 0; left &= left - 1) {
+        const int key = key0 + own + (int)__builtin_ctzll(left), pg = page_of(key);
         if (pg < 0 || key > lim) continue;
         const _Float16* v = a.v_cache +
             (((int64_t)pg * a.Hkv + h) * a.page_size + (key & (a.page_size - 1))) * D + 4 * half;
@@ -710,6 +721,36 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
   l = sum_halves(l);
+  if constexpr (KS == 2) {
+    // the second group's sums join the first's through LDS, a lane's to the same lane's
+    const uint32_t to = ring + row_wave * (D * 128) + lane * 16;
+    float* ml = s_ml[row_wave][0] + lane;
+    __syncthreads();                       // the ring has been read
+    if (key_wave == 1) {
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          lds_put(to + (4 * d + g) * 1024,
+                  f32x4{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]});
+      ml[0] = m;
+      ml[64] = l;
+    }
+    __syncthreads();
+    if (key_wave == 1) return;
+    const float m1 = ml[0], mn = fmaxf(m, m1), mu = mn == -INFINITY ? 0.f : mn;
+    const float f0 = __builtin_amdgcn_exp2f(m - mu), f1 = __builtin_amdgcn_exp2f(m1 - mu);
+    m = mn;
+    l = l * f0 + ml[64] * f1;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 y = lds_get<f32x4>(to + (4 * d + g) * 1024);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[d][4 * g + e] = o[d][4 * g + e] * f0 + y[e] * f1;
+      }
+  }
   if (wr0 + col >= nrows) return;
   if (splits == 1) {
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
@@ -726,7 +767,7 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW>::kPerSimd)) void attn_til
   } else {
     const int64_t item = (((int64_t)b * a.Hkv + h) * gridDim.y + tile) * splits + split;
     float* po = part + item * kTileRows * (D + 2);
-    const int r = 32 * wave + col;
+    const int r = 32 * row_wave + col;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -808,9 +849,9 @@ void launch_stream(const AttnArgs& a, const AttnPlan& p, unsigned* tickets, floa
                      dim3(kThreads), 0, stream, a, p.splits, tickets, partials);
 }
 
-template <int D, int NW>
+template <int D, int NW, int KS>
 void launch_tile(const AttnArgs& a, const AttnPlan& p, float* partials, hipStream_t stream) {
-  hipLaunchKernelGGL((attn_tile_kernel<D, NW>), dim3(a.Hkv * p.splits, p.row_tiles, a.B),
+  hipLaunchKernelGGL((attn_tile_kernel<D, NW, KS>), dim3(a.Hkv * p.splits, p.row_tiles, a.B),
                      dim3(64 * NW), 0, stream, a, p.splits, partials);
 }
 
@@ -820,9 +861,9 @@ void launch_d(const AttnArgs& a, const AttnPlan& p, void* ws, hipStream_t stream
   float* partials = reinterpret_cast<float*>(static_cast<char*>(ws) + kTicketRegion);
   if (p.rows == 16) launch_stream<D, 1>(a, p, tickets, partials, stream);
   else if (p.rows == 32) launch_stream<D, 2>(a, p, tickets, partials, stream);
-  else if (p.rows == 64) launch_tile<D, 2>(a, p, partials, stream);
-  else if (p.rows == 128) launch_tile<D, 4>(a, p, partials, stream);
-  else if constexpr (D != 256) launch_tile<D, 8>(a, p, partials, stream);
+  else if (p.rows == 64) launch_tile<D, D == 256 ? 2 : 4, D == 256 ? 1 : 2>(a, p, partials, stream);
+  else if (p.rows == 128) launch_tile<D, 4, 1>(a, p, partials, stream);
+  else if constexpr (D != 256) launch_tile<D, 8, 1>(a, p, partials, stream);
   if (p.splits > 1 && !p.last_joins)
     hipLaunchKernelGGL(attn_join_kernel<D>, dim3((a.max_q * a.Hq + 3) / 4, a.B), dim3(256), 0,
                        stream, a, p.splits, p.row_tiles, p.rows, partials);
@@ -840,13 +881,18 @@ AttnPlan plan_attention(int B, int max_q, int max_ctx, int Hq, int Hkv, int D) {
   const int64_t items = (int64_t)B * Hkv * p.row_tiles;
   const int tiles = (max_ctx + 31) / 32;
   // While there are fewer row tiles than the CUs hold blocks, contexts are split: down to 8 tiles of 32
-  // keys a block, and while every block has a CU of its own down to 4 (2 for more than 32 rows, whose
-  // blocks have two waves).  us, one token a sequence, 8 key heads: 4 sequences of 8,192 tokens on 256 /
-  // 512 / 1,024 blocks 27 / 32 / 48; 1 of 1,001 in splits of 2 / 4 / 8 / 16 tiles 8.7 / 8.0 / 9.2 / 11.
-  // 16 tokens a sequence: 8 of 8,213 on 256 / 512 / 1,024 blocks 67 / 49 / 59; 1 of 1,016 in splits of
-  // 1 / 2 / 4 / 8 / 16 tiles 10.9 / 10.4 / 11.7 / 14.9 / 21.
+  // keys a block, and while every block has a CU of its own down to 4 (2 for more than 32 rows).  us,
+  // one token a sequence, 8 key heads: 4 sequences of 8,192 tokens on 256 / 512 / 1,024 blocks 27 / 32 /
+  // 48; 1 of 1,001 in splits of 2 / 4 / 8 / 16 tiles 8.7 / 8.0 / 9.2 / 11.  21 tokens a sequence: 8 of
+  // 3,000 in splits of 12 / 23 tiles 31 / 34.  16 tokens: 1 of 1,016 in splits of 1 / 2 / 4 / 8 / 16
+  // tiles 10.9 / 10.4 / 11.7 / 14.9 / 21.
+  // Where most CUs have a block already, the partial results cost more than splits shorter than 32
+  // tiles give: 32 sequences of 16 tokens (256 row tiles) over 500 / 1,016 / 2,000 tokens split in two
+  // 30 / 38 / 58, unsplit 21 / 30 / 53; 22 (176) 25 / 32 / 43 and 19 / 29 / 48; 16 (128) of 1,016 /
+  // 2,000 in four 26 / 34, in two 27 / 36.
   const int blocks = p.rows <= 32 || (p.rows == 256 && D == 128) ? 256 : 512;
-  int64_t splits = items < blocks ? std::min<int64_t>(blocks / items, tiles / 8) : 1;
+  const int shortest = items <= 160 ? 8 : 32;
+  int64_t splits = items < blocks ? std::min<int64_t>(blocks / items, tiles / shortest) : 1;
   if (items < 256)
     splits = std::max(splits, std::min<int64_t>(256 / items, tiles / (p.rows <= 32 ? 4 : 2)));
   // Many long sequences, seldom of one length: splits of 128 tiles and more, up to 2,048 blocks, even
