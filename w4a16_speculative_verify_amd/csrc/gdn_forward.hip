@@ -36,9 +36,9 @@
 // the products as pairs of fp16, hi + lo with 22 bits, three products of pairs or
 // two with an fp16 operand: the state keeps fp32's accuracy (3 to 5e-7 of its length
 // after 8,192 tokens; with hi alone 2^-12 a product would stay in it).
-//   8,192 tokens x 16 heads of 128: 197 us (38 the chunks, 163 the scan, 1.3 us a
+//   8,192 tokens x 16 heads of 128: 191 us (33 the chunks, 161 the scan, 1.3 us a
 //   chunk on the chain of dependent small products); 4 x 2,048 ragged tokens x 16
-//   heads of 64: 63 us.
+//   heads of 64: 60 us.
 #include "w4v_device.h"
 #include "w4v_launch.h"
 
@@ -370,16 +370,20 @@ __device__ __forceinline__ Pair t_beta(const float* t, const float* beta) {
 // formed transposed, with rows and columns in tau order, so that a lane's
 // accumulators are the eight consecutive values of a fragment: scale R (q.k) goes
 // from registers to the workspace, L through LDS into the inversion.  K and Q
-// make room for L and T once they have been read: 42 KiB a block, three blocks a
-// CU, which hide the chain of small steps (loads, products, inversion).
+// make room for L and T once they have been read: 39 KiB a block, four blocks a CU (33 us for
+// 8,192 tokens x 16 heads of 128, three blocks 38), which hide the chain of small steps (loads,
+// products, inversion).
 template <int D>
 __global__ __launch_bounds__(256) void gdn_chunk_kernel(GdnArgs a, char* __restrict__ ws) {
   constexpr int DS = D / 32;
   constexpr int kRowsF = kC * D;                       // K and Q as fp16: D floats a row pair
   constexpr int kTiles = 2 * kC * kLd;                 // L and T
   __shared__ __attribute__((aligned(16))) float s_buf[kRowsF > kTiles ? kRowsF : kTiles];
-  __shared__ float s_m[4][16 * 17];
-  __shared__ __attribute__((aligned(16))) float s_alpha[kC], s_beta[kC], s_end[kC][9];
+  __shared__ __attribute__((aligned(16))) float s_alpha[kC], s_beta[kC], s_small[4 * 16 * 17];
+  // the gates' products until the decays are taken, then the inversion's scratch
+  float (*s_end)[9] = reinterpret_cast<float (*)[9]>(s_small);
+  float (*s_m)[16 * 17] = reinterpret_cast<float (*)[16 * 17]>(s_small);
+  static_assert(kC * 9 <= 4 * 16 * 17, "the gates' products exceed the scratch");
   _Float16* s_k = reinterpret_cast<_Float16*>(s_buf);
   _Float16* s_q = s_k + kC * D;
   float* s_l = s_buf;
