@@ -33,13 +33,16 @@
 // the 32 x 32 instruction, one barrier a tile.  64 rows take four waves, two for either half of a
 // tile's keys, joined in LDS: with two waves alone the CU waits for the chain of one (32 sequences x
 // 8 tokens over 8,208, D = 64, 80 -> 54 us; 64 x 16 over 8,208, D = 128, 376 -> 365; 128 rows lose,
-// 411 -> 476, and D = 256 has the registers for one wave a SIMD, 61 -> 80).  Verify blocks are bound by the bytes
-// again (8 x 21 rows over 8,213 tokens 49 us, 4.2 TB/s), prompts by the matrix cores and the conversions
-// beside them: 8,192 tokens 32 / 8 heads of 128 575 us, 956 TFLOP/s, where a loop of nothing but these
-// matrix instructions reaches 1,330-1,550 on this card (the clock falls to 2.0 GHz) and one with seven
-// vector instructions a product, about this kernel's mix, 1,120-1,190.  Scores of the next tile
-// computed beside this one's weights, values read ahead, two blocks of four waves a CU and other wave
-// priorities took 7-12 %, 4 %, 3 % and 0 % longer than this form, timed in turn.
+// 411 -> 476, and D = 256 has the registers for one wave a SIMD, 61 -> 80).
+//   Verify blocks are bound by the bytes again, the partial results' among them: 8 x 21 rows over 8,213
+//   tokens 62 us from HBM (202 MB, and 44 of partials), 48 where the cache is in the last-level cache;
+//   1 x 16 over 8,208 21 us, of which 2 pass before the first copy, 3 before it lands and 4 in the join.
+//   Prompts are bound by the matrix cores and the conversions beside them: 8,192 tokens, 32 / 8 heads
+//   of 128, 575 us, 956 TFLOP/s, where a loop of nothing but these matrix instructions reaches
+//   1,330-1,550 on this card (the clock falls to 2.0 GHz) and one with seven vector instructions a
+//   product, about this kernel's mix, 1,120-1,190.  Scores of the next tile computed beside this
+//   one's weights, values read ahead, two blocks of four waves a CU and other wave priorities took
+//   7-12 %, 4 %, 3 % and 0 % longer than this form, timed in turn.
 //
 // Contexts are split over blocks where rows are few (plan_attention); partial sums (fp32, with m and l)
 // are joined in the splits' order, by the row tile's last block when they are few, else by
@@ -886,12 +889,12 @@ AttnPlan plan_attention(int B, int max_q, int max_ctx, int Hq, int Hkv, int D) {
   // 48; 1 of 1,001 in splits of 2 / 4 / 8 / 16 tiles 8.7 / 8.0 / 9.2 / 11.  21 tokens a sequence: 8 of
   // 3,000 in splits of 12 / 23 tiles 31 / 34.  16 tokens: 1 of 1,016 in splits of 1 / 2 / 4 / 8 / 16
   // tiles 10.9 / 10.4 / 11.7 / 14.9 / 21.
-  // Where most CUs have a block already, the partial results cost more than splits shorter than 32
-  // tiles give: 32 sequences of 16 tokens (256 row tiles) over 500 / 1,016 / 2,000 tokens split in two
-  // 30 / 38 / 58, unsplit 21 / 30 / 53; 22 (176) 25 / 32 / 43 and 19 / 29 / 48; 16 (128) of 1,016 /
-  // 2,000 in four 26 / 34, in two 27 / 36.
+  // Where most CUs have a block already, the partial results cost more than short splits give: 32
+  // sequences of 16 tokens (256 row tiles) over 500 / 1,016 / 2,000 tokens split in two 30 / 38 / 58,
+  // unsplit 21 / 30 / 53; 30 of 32 (240) over 1,600 68 and 64; 22 (176) over 500 / 1,016 / 2,000 25 /
+  // 32 / 43 and 19 / 29 / 48; 16 (128) of 1,016 / 2,000 in four 26 / 34, in two 27 / 36.
   const int blocks = p.rows <= 32 || (p.rows == 256 && D == 128) ? 256 : 512;
-  const int shortest = items <= 160 ? 8 : 32;
+  const int shortest = items <= 160 ? 8 : items <= 224 ? 20 : 32;
   int64_t splits = items < blocks ? std::min<int64_t>(blocks / items, tiles / shortest) : 1;
   if (items < 256)
     splits = std::max(splits, std::min<int64_t>(256 / items, tiles / (p.rows <= 32 ? 4 : 2)));
