@@ -231,10 +231,12 @@ __device__ __forceinline__ int swz(int r) {
 // Eight fp32 values (two accumulators' lanes) as fp16 pairs x = hi + lo.  The
 // values are fixed in registers first: a product or sum that the compiler
 // rounded to fp16 once for hi and through fp32 for lo would give a lo that
-// belongs to another hi where the two roundings differ.
+// belongs to another hi where the two roundings differ.  What a matrix
+// instruction gave is in registers already (kFix = false: no copies).
 struct Pair {
   f16x8 hi, lo;
 };
+template <bool kFix = true>
 __device__ __forceinline__ Pair split(const f32x4& x, const f32x4& y) {
   Pair p;
   float minus = -1.f;                      // hidden: lo is one mixed-precision fma per value
@@ -242,7 +244,7 @@ __device__ __forceinline__ Pair split(const f32x4& x, const f32x4& y) {
 #pragma unroll
   for (int e = 0; e < 8; e += 2) {
     float v = e < 4 ? x[e & 3] : y[e & 3], w = e < 4 ? x[(e & 3) + 1] : y[(e & 3) + 1];
-    asm("" : "+v"(v), "+v"(w));
+    if constexpr (kFix) asm("" : "+v"(v), "+v"(w));
     f16x2 h = {(_Float16)v, (_Float16)w};
     asm("" : "+v"(h));                     // one conversion serves hi and the remainder
     p.hi[e] = h[0];
@@ -851,7 +853,7 @@ __global__ __launch_bounds__(64 * (3 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
     const uint32_t gh = go + 32 * hf * 4;
     const uint32_t vh = lds + L::kV + ((8 * grp + 32 * hf) * NV * 16 + tile * 16 + col) * 2;
     const auto publish = [&](int s) {
-      sp[s] = split(st[2 * s], st[2 * s + 1]);
+      sp[s] = split<false>(st[2 * s], st[2 * s + 1]);
       lds_put(so + s * 2 * kFragBytes, sp[s].hi);
       lds_put(so + (s * 2 + 1) * kFragBytes, sp[s].lo);
     };
@@ -860,25 +862,16 @@ __global__ __launch_bounds__(64 * (3 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
     for (int c = 0; c < chunks; ++c) {
       const uint32_t buf = (c & 1) * L::kBuf;
       lds_barrier();
-      // ---- X over the half's dk: the other half's tokens first
-      f32x4 x[2][2];
+      // all reads of the chunk that need no result of it go out first
+      f16x8 kx[2][HS][2];                  // K of the other half's tokens, then of the own
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        const uint32_t po = buf + (p == 0 ? 1 - hf : hf) * kTile[2];
-        x[p][0] = x[p][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int s = 0; s < HS; ++s) {
-          const f16x8 k0 = at(rh[s] + po), k1 = at(rh[s] + po + kTile[1]);
-          x[p][0] = mfma16x16x32(k0, sp[s].hi, x[p][0]);
-          x[p][1] = mfma16x16x32(k1, sp[s].hi, x[p][1]);
-          x[p][0] = mfma16x16x32(k0, sp[s].lo, x[p][0]);
-          x[p][1] = mfma16x16x32(k1, sp[s].lo, x[p][1]);
+          const uint32_t po = buf + (p == 0 ? 1 - hf : hf) * kTile[2];
+          kx[p][s][0] = at(rh[s] + po);
+          kx[p][s][1] = at(rh[s] + po + kTile[1]);
         }
-      }
-      const uint32_t xw = xo + (1 - hf) * 2 * kFragBytes, xr = xo + hf * 2 * kFragBytes;
-      lds_put(xw, x[0][0]);
-      lds_put(xw + kFragBytes, x[0][1]);
-      // what E needs besides
       f32x4 g[2], d[4], e[2];
       _Float16 v[2][4];
       f16x8 th[4], tl[4];                  // half 0: tiles 0 .. 3 at s = 0; half 1: tiles 2, 3 at s = 1
@@ -901,7 +894,6 @@ __global__ __launch_bounds__(64 * (3 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
           tl[i] = at(fo + buf + L::kF + (frag_of(2 + i, 1) * 2 + 1) * kFragBytes);
         }
       }
-      // ---- S': what does not need U
       f16x8 k[HS][2][2];
 #pragma unroll
       for (int s = 0; s < HS; ++s)
@@ -913,6 +905,24 @@ __global__ __launch_bounds__(64 * (3 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
             const uint32_t o = ko[s] + buf + 32 * p * D * 2 + 8 * m;
             k[s][p][m] = join8(lds_get_tr(o), lds_get_tr(o + 4 * D * 2));
           }
+      __builtin_amdgcn_sched_barrier(0);
+      // ---- X over the half's dk: the other half's tokens first
+      f32x4 x[2][2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        x[p][0] = x[p][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < HS; ++s)
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              x[p][i] = mfma16x16x32(kx[p][s][i], y == 0 ? sp[s].hi : sp[s].lo, x[p][i]);
+      }
+      const uint32_t xw = xo + (1 - hf) * 2 * kFragBytes, xr = xo + hf * 2 * kFragBytes;
+      lds_put(xw, x[0][0]);
+      lds_put(xw + kFragBytes, x[0][1]);
+      // ---- S': what does not need U
       const float gc = lds_get<float>(lds + buf + L::kGate + (kC - 1) * 4);
 #pragma unroll
       for (int m = 0; m < 2 * HS; ++m)
