@@ -36,9 +36,9 @@
 // the products as pairs of fp16, hi + lo with 22 bits, three products of pairs or
 // two with an fp16 operand: the state keeps fp32's accuracy (3 to 5e-7 of its length
 // after 8,192 tokens; with hi alone 2^-12 a product would stay in it).
-//   8,192 tokens x 16 heads of 128: 191 us (33 the chunks, 161 the scan, 1.3 us a
+//   8,192 tokens x 16 heads of 128: 178 us (33 the chunks, 147 the scan, 1.15 us a
 //   chunk on the chain of dependent small products); 4 x 2,048 ragged tokens x 16
-//   heads of 64: 60 us.
+//   heads of 64: 57 us.
 #include "w4v_device.h"
 #include "w4v_launch.h"
 
@@ -236,14 +236,14 @@ __device__ __forceinline__ int swz(int r) {
 struct Pair {
   f16x8 hi, lo;
 };
-template <bool kFix = true>
-__device__ __forceinline__ Pair split(const f32x4& x, const f32x4& y) {
+template <bool kFix, typename F>
+__device__ __forceinline__ Pair split_of(F f) {      // of f(0) .. f(7)
   Pair p;
   float minus = -1.f;                      // hidden: lo is one mixed-precision fma per value
   asm("" : "+v"(minus));
 #pragma unroll
   for (int e = 0; e < 8; e += 2) {
-    float v = e < 4 ? x[e & 3] : y[e & 3], w = e < 4 ? x[(e & 3) + 1] : y[(e & 3) + 1];
+    float v = f(e), w = f(e + 1);
     if constexpr (kFix) asm("" : "+v"(v), "+v"(w));
     f16x2 h = {(_Float16)v, (_Float16)w};
     asm("" : "+v"(h));                     // one conversion serves hi and the remainder
@@ -253,6 +253,14 @@ __device__ __forceinline__ Pair split(const f32x4& x, const f32x4& y) {
     p.lo[e + 1] = (_Float16)__builtin_fmaf((float)h[1], minus, w);
   }
   return p;
+}
+template <bool kFix = true>
+__device__ __forceinline__ Pair split(const f32x4& x, const f32x4& y) {
+  return split_of<kFix>([&](int e) { return e < 4 ? x[e & 3] : y[e & 3]; });
+}
+// of products, whose results then need no place in a vector
+__device__ __forceinline__ Pair split_products(const f32x4* x, const f32x4* y) {
+  return split_of<true>([&](int e) { return x[e >> 2][e & 3] * y[e >> 2][e & 3]; });
 }
 
 // ROWS rows of D fp16 from global (row stride ld) into an LDS tile, by NT threads; rows at or past n
@@ -872,7 +880,9 @@ __global__ __launch_bounds__(64 * (3 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
           kx[p][s][0] = at(rh[s] + po);
           kx[p][s][1] = at(rh[s] + po + kTile[1]);
         }
-      f32x4 g[2], d[4], e[2];
+      __builtin_amdgcn_sched_barrier(0);
+      const float gc = lds_get<float>(lds + buf + L::kGate + (kC - 1) * 4);
+      f32x4 g[2], d[4];
       _Float16 v[2][4];
       f16x8 th[4], tl[4];                  // half 0: tiles 0 .. 3 at s = 0; half 1: tiles 2, 3 at s = 1
 #pragma unroll
@@ -905,7 +915,6 @@ __global__ __launch_bounds__(64 * (3 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
             const uint32_t o = ko[s] + buf + 32 * p * D * 2 + 8 * m;
             k[s][p][m] = join8(lds_get_tr(o), lds_get_tr(o + 4 * D * 2));
           }
-      __builtin_amdgcn_sched_barrier(0);
       // ---- X over the half's dk: the other half's tokens first
       f32x4 x[2][2];
 #pragma unroll
@@ -923,12 +932,14 @@ __global__ __launch_bounds__(64 * (3 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
       lds_put(xw, x[0][0]);
       lds_put(xw + kFragBytes, x[0][1]);
       // ---- S': what does not need U
-      const float gc = lds_get<float>(lds + buf + L::kGate + (kC - 1) * 4);
 #pragma unroll
       for (int m = 0; m < 2 * HS; ++m)
 #pragma unroll
         for (int r = 0; r < 4; ++r) st[m][r] *= gc;
       lds_barrier();
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) d[tt] = lds_get<f32x4>(go + buf + (kC + kTok[tt]) * 4);
+      f32x4 e[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const f32x4 y = lds_get<f32x4>(xr + i * kFragBytes);
@@ -938,24 +949,23 @@ __global__ __launch_bounds__(64 * (3 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
       const Pair ep = split(e[0], e[1]);
       // ---- U: half 0 gives tokens 0 .. 31 and one addend of 32 .. 63, half 1 the other
       f32x4 u[4];
-      const auto te = [&](int i, f32x4& y) {
-        y = mfma16x16x32(th[i], ep.hi, f32x4{0.f, 0.f, 0.f, 0.f});
-        y = mfma16x16x32(tl[i], ep.hi, y);
-        y = mfma16x16x32(th[i], ep.lo, y);
+      const auto te = [&](auto n, f32x4* y) {          // tiles side by side
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+#pragma unroll
+          for (int i = 0; i < decltype(n)::value; ++i)
+            y[i] = mfma16x16x32(x == 1 ? tl[i] : th[i], x == 2 ? ep.lo : ep.hi,
+                                x == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : y[i]);
       };
       if (hf == 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) te(i, u[i]);
+        te(std::integral_constant<int, 4>(), u);
 #pragma unroll
         for (int i = 0; i < 4; ++i) lds_put(uo + i * kFragBytes, u[i]);
       } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) te(i, u[2 + i]);
+        te(std::integral_constant<int, 2>(), u + 2);
 #pragma unroll
         for (int i = 0; i < 2; ++i) lds_put(uo + (4 + i) * kFragBytes, u[2 + i]);
       }
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt) d[tt] = lds_get<f32x4>(go + buf + (kC + kTok[tt]) * 4);
       lds_barrier();
       if (hf == 0) {
 #pragma unroll
@@ -969,11 +979,7 @@ __global__ __launch_bounds__(64 * (3 * NV + 1), 1) void gdn_scan_kernel(GdnArgs 
       }
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) u[2 * p + i][r] *= d[2 * p + i][r];
-        const Pair up = split(u[2 * p], u[2 * p + 1]);
+        const Pair up = split_products(u + 2 * p, d + 2 * p);
 #pragma unroll
         for (int m = 0; m < 2 * HS; ++m) st[m] = mfma16x16x32(k[m >> 1][p][m & 1], up.hi, st[m]);
 #pragma unroll
