@@ -911,9 +911,10 @@ AttnPlan plan_attention(int B, int max_q, int max_ctx, int Hq, int Hkv, int D) {
   // Where most CUs have a block already, the partial results cost more than short splits give: 32
   // sequences of 16 tokens (256 row tiles) over 500 / 1,016 / 2,000 tokens split in two 30 / 38 / 58,
   // unsplit 21 / 30 / 53; 30 of 32 (240) over 1,600 68 and 64; 22 (176) over 500 / 1,016 / 2,000 25 /
-  // 32 / 43 and 19 / 29 / 48; 16 (128) of 1,016 / 2,000 in four 26 / 34, in two 27 / 36.
+  // 32 / 43 and 19 / 29 / 48; 16 (128) of 1,016 / 2,000 in four 26 / 34, in two 27 / 36.  Tiles of 256
+  // rows bring more of them: 2 x 1,000 tokens over 4,000 (256 row tiles, D = 64) in two 110, unsplit 85.
   const int blocks = p.rows <= 32 || (p.rows == 256 && D == 128) ? 256 : 512;
-  const int shortest = items <= 160 ? 8 : items <= 224 ? 20 : 32;
+  const int shortest = items <= 160 ? 8 : items <= 224 ? 20 : p.rows == 256 ? 128 : 32;
   int64_t splits = items < blocks ? std::min<int64_t>(blocks / items, tiles / shortest) : 1;
   if (items < 256)
     splits = std::max(splits, std::min<int64_t>(256 / items, tiles / (p.rows <= 32 ? 4 : 2)));
@@ -921,7 +922,14 @@ AttnPlan plan_attention(int B, int max_q, int max_ctx, int Hq, int Hkv, int D) {
   // out what the CUs get (64 ragged sequences up to 16,384 tokens 527 -> 480 us; shorter splits cost
   // more than they give, 64 of 2,048 tokens 98 unsplit, 110 in two).
   if (p.rows <= 32 && items >= blocks) splits = std::min<int64_t>(2048 / items, tiles / 128);
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(64, splits));
+  splits = std::max<int64_t>(1, std::min<int64_t>(64, splits));
+  // 256 rows: what the splits save, 0.55 us (D = 64) or 0.85 (128) a tile of 32 keys, against the
+  // partial results, 0.04 us a block, and the join's launch.  Unsplit / split: 1,000 tokens of a prompt
+  // 34 / 43 us, over 4,000 112 / 90, 100 over 500 22 / 17, 100 over 200 13.5 / 15; D = 64: 1,000 25 / 38,
+  // over 4,000 79 / 60, 4 x 300 over 700 20 / 45, 60 over 1,000 25 / 15.
+  if (p.rows == 256 && tiles * (1 - 1.0 / splits) * (0.25 + 0.0047 * D) < 4 + 0.04 * items * splits)
+    splits = 1;
+  p.splits = (int)splits;
   p.last_joins = p.rows <= 32 && std::min<int64_t>(rows, p.rows) * p.splits <= 128 &&
                  items * kJoinStride * sizeof(unsigned) <= kTicketRegion;
   p.workspace = p.splits == 1 ? 0 : kTicketRegion + (size_t)items * p.splits * p.rows * (D + 2) * sizeof(float);
