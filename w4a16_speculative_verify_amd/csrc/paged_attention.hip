@@ -923,12 +923,18 @@ AttnPlan plan_attention(int B, int max_q, int max_ctx, int Hq, int Hkv, int D) {
   // more than they give, 64 of 2,048 tokens 98 unsplit, 110 in two).
   if (p.rows <= 32 && items >= blocks) splits = std::min<int64_t>(2048 / items, tiles / 128);
   splits = std::max<int64_t>(1, std::min<int64_t>(64, splits));
-  // 256 rows: what the splits save, 0.55 us (D = 64) or 0.85 (128) a tile of 32 keys, against the
-  // partial results, 0.04 us a block, and the join's launch.  Unsplit / split: 1,000 tokens of a prompt
-  // 34 / 43 us, over 4,000 112 / 90, 100 over 500 22 / 17, 100 over 200 13.5 / 15; D = 64: 1,000 25 / 38,
-  // over 4,000 79 / 60, 4 x 300 over 700 20 / 45, 60 over 1,000 25 / 15.
-  if (p.rows == 256 && tiles * (1 - 1.0 / splits) * (0.25 + 0.0047 * D) < 4 + 0.04 * items * splits)
-    splits = 1;
+  // Short contexts: what the splits save, per_tile us for 32 keys of a block, against the partial
+  // results and the join (both fitted to the times below, within 20 %).  Unsplit / split, us: 8 key
+  // heads of 128, 32 rows: 8 x 8 tokens over 300 12 / 15, over 800 18 / 17; 64 rows: 16 x 16 over 300
+  // 11 / 17, 1 x 16 over 300 11.1 / 10.5; 128 rows: 16 x 32 over 300 14 / 24, 1 x 32 over 400 16 / 13;
+  // 256 rows: 1,000 tokens of a prompt 34 / 43, over 4,000 112 / 90, 100 over 500 22 / 17; 4 heads of 64,
+  // 256 rows: 1,000 tokens 25 / 38, over 4,000 79 / 60, 4 x 300 over 700 20 / 45.  16 rows, whose partial
+  // results are few, are split in any case.
+  if (p.rows > 16) {
+    const double per_tile = (D == 256 && p.rows > 32 ? 2.4 : 0.25 + 0.0047 * D) * (0.45 + 0.00215 * p.rows);
+    const double join = 2.5 + 0.006 * p.rows + items * splits * (0.012 + 0.00011 * p.rows);
+    if (tiles * (1 - 1.0 / splits) * per_tile < join) splits = 1;
+  }
   p.splits = (int)splits;
   p.last_joins = p.rows <= 32 && std::min<int64_t>(rows, p.rows) * p.splits <= 128 &&
                  items * kJoinStride * sizeof(unsigned) <= kTicketRegion;
