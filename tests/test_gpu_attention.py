@@ -146,7 +146,7 @@ def test_later_positions_may_hold_anything(lib, new, d):
     assert np.all(np.isfinite(got[new:]))
 
 
-@pytest.mark.parametrize("new", [1, 4, 9, 40])
+@pytest.mark.parametrize("new", [1, 4, 9, 20, 40])
 def test_nan_queries_and_keys_reach_their_rows(lib, new):
     """A query of NaN, and a stretch of keys of NaN that fills whole splits, show in the rows that they
     belong to, whichever blocks share the context, and nowhere else."""

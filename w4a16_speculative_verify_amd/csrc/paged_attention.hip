@@ -38,7 +38,7 @@
 //   tokens 62 us from HBM (202 MB, and 44 of partials), 48 where the cache is in the last-level cache;
 //   1 x 16 over 8,208 21 us, of which 2 pass before the first copy, 3 before it lands and 4 in the join.
 //   Prompts are bound by the matrix cores and the conversions beside them: 8,192 tokens, 32 / 8 heads
-//   of 128, 575 us, 956 TFLOP/s, where a loop of nothing but these matrix instructions reaches
+//   of 128, 557 us, 987 TFLOP/s, where a loop of nothing but these matrix instructions reaches
 //   1,330-1,550 on this card (the clock falls to 2.0 GHz) and one with seven vector instructions a
 //   product, about this kernel's mix, 1,120-1,190.  Scores of the next tile computed beside this
 //   one's weights, values read ahead, two blocks of four waves a CU and other wave priorities took
