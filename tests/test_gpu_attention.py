@@ -403,6 +403,21 @@ def test_the_context_hint_shapes_the_launch_only(lib, new, max_ctx):
     run_attention(lib, x, max_ctx=max_ctx)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_splits_of_many_rows_are_joined(lib, d):
+    """A chunk shaped for thousands of rows (of which few are there) over a context in two to four
+    splits: several rows a wave are joined, the last of them alone."""
+    rng = np.random.default_rng(d)
+    x = gen.paged_batch(rng, [131, 3], [2990, 1200], 8, 1, d, 64, pad_rows=2)
+    args = [dev(a) for a in (x.q, x.k_cache, x.v_cache, x.table, x.cu, x.ctx)]
+    out = dev(np.full(x.q.shape, 7.0, np.float16))
+    assert lib.paged_attention_workspace_size(2, 2000, 3000, 8, 1, d) > 0
+    got = host(lib.paged_attention(*args, 2000, 3000, out=out))
+    ref = oa.attention(x.q, x.k_cache, x.v_cache, x.table, x.cu, x.ctx, d ** -0.5)
+    check_attention(got, x.q, ref, d, d ** -0.5, "attention")
+    assert np.all(got[134:] == 7.0)
+
+
 def test_rows_past_max_q_are_left(lib):
     import torch
     rng = np.random.default_rng(16)

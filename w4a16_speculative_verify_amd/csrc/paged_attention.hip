@@ -803,65 +803,97 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW, KS>::kPerSimd)) void attn
   }
 }
 
-// Joins the splits of one (token, query head) per wave: 64 / (D / 4) splits a load, the loads of
-// eight rounds in flight before the weights are known.  (32 splits of 512 rows of 128: one split a
-// load, eight in flight, took 11 us.)
-template <int D>
+// Joins the splits of (token, query head)s, N = 8 / U of them a wave: 64 / (D / 4) splits a load, U
+// loads a round of a row, so that eight are in flight before the weights are known.  Bound by the
+// latency of two dependent loads (4 us for 512 rows) and, with many rows, by the partial results' bytes.
+template <int D, int U>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int splits, int row_tiles, int R,
                                                         const float* __restrict__ part) {
-  constexpr int LR = D / 4, SP = 64 / LR;      // lanes a row, splits a load
+  constexpr int LR = D / 4, SP = 64 / LR, N = 8 / U;      // lanes a row, splits a load, rows
   const int lane = threadIdx.x & 63;
-  const int y = blockIdx.x * 4 + (threadIdx.x >> 6), b = blockIdx.y;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int y0 = (blockIdx.x * 4 + wave) * N, b = blockIdx.y;
   const Seq sq = seq_of(a, b);
-  const int G = a.Hq / a.Hkv;
-  const int i = y / a.Hq, head = y % a.Hq;
-  if (i >= sq.T) return;
-  const int h = head / G, x = i * G + head % G, tile = x / R, r = x % R;
-  const float* base = part + (((int64_t)b * a.Hkv + h) * row_tiles + tile) * splits * R * (D + 2);
+  const int G = a.Hq / a.Hkv, rows = sq.T * a.Hq;
+  if (y0 >= rows) return;
   const int64_t step = (int64_t)R * (D + 2);
-  float ms = -INFINITY, ls = 0.f;
-  if (lane < splits) {
-    const f32x2 ml = *reinterpret_cast<const f32x2*>(base + lane * step + R * D + 2 * r);
-    ms = ml[0];
-    ls = ml[1];
-  }
-  const float* p = base + (int64_t)r * D + 4 * (lane % LR);
-  f32x4 acc{0.f, 0.f, 0.f, 0.f};
-  float f = 0.f, sum = 0.f;
-  for (int s0 = 0; s0 < splits; s0 += 8 * SP) {
-    f32x4 v[8];
+  const float* p[N];
+  float ms[N], ls[N];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      v[k] = *reinterpret_cast<const f32x4*>(p + min(s0 + k * SP + lane / LR, splits - 1) * step);
-    if (s0 == 0) {
-      float mx = ms;
-#pragma unroll
-      for (int k = 1; k < 64; k <<= 1) mx = fmaxf(mx, __shfl_xor(mx, k, 64));
-      f = ms == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms - mx);
-      sum = f * ls;
-#pragma unroll
-      for (int k = 1; k < 64; k <<= 1) sum += __shfl_xor(sum, k, 64);
+  for (int n = 0; n < N; ++n) {
+    const int y = min(y0 + n, rows - 1), i = y / a.Hq, head = y % a.Hq;
+    const int h = head / G, x = i * G + head % G, tile = x / R, r = x % R;
+    const float* base = part + (((int64_t)b * a.Hkv + h) * row_tiles + tile) * splits * step;
+    ms[n] = -INFINITY;
+    ls[n] = 0.f;
+    if (lane < splits) {
+      const f32x2 ml = *reinterpret_cast<const f32x2*>(base + lane * step + R * D + 2 * r);
+      ms[n] = ml[0];
+      ls[n] = ml[1];
     }
+    p[n] = base + (int64_t)r * D + 4 * (lane % LR);
+  }
+  f32x4 acc[N];
+  float f[N], sum[N];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int s = s0 + k * SP + lane / LR;
-      const float w = __shfl(f, s & 63, 64);
-      if (s < splits) {
+  for (int n = 0; n < N; ++n) {
+    acc[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f[n] = sum[n] = 0.f;
+  }
+  for (int s0 = 0; s0 < splits; s0 += U * SP) {
+    f32x4 v[N][U];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(w, v[k][e], acc[e]);
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        v[n][k] = *reinterpret_cast<const f32x4*>(
+            p[n] + min(s0 + k * SP + lane / LR, splits - 1) * step);
+    if (s0 == 0) {
+      // lanes behind the splits hold none: the sums of the first lanes are whole
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        float mx = ms[n];
+        for (int k = 1; k < splits; k <<= 1) mx = fmaxf(mx, __shfl_xor(mx, k, 64));
+        f[n] = ms[n] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ms[n] - mx);
+        sum[n] = f[n] * ls[n];
+        for (int k = 1; k < splits; k <<= 1) sum[n] += __shfl_xor(sum[n], k, 64);
+        sum[n] = __shfl(sum[n], 0, 64);
       }
     }
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int s = s0 + k * SP + lane / LR;
+        const float w = __shfl(f[n], s & 63, 64);
+        if (s < splits) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[n][e] = __builtin_fmaf(w, v[n][k][e], acc[n][e]);
+        }
+      }
   }
 #pragma unroll
-  for (int k = LR; k < 64; k <<= 1)
+  for (int n = 0; n < N; ++n) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] += __shfl_xor(acc[e], k, 64);
-  if (lane >= LR) return;
-  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-  f16x4 o;
+    for (int k = LR; k < 64; k <<= 1)
 #pragma unroll
-  for (int e = 0; e < 4; ++e) o[e] = (_Float16)(acc[e] * inv);
-  *reinterpret_cast<f16x4*>(a.out + (int64_t)(sq.start + i) * a.ldo + (int64_t)head * D + 4 * lane) = o;
+      for (int e = 0; e < 4; ++e) acc[n][e] += __shfl_xor(acc[n][e], k, 64);
+    const int y = y0 + n;
+    if (lane >= LR || y >= rows) continue;
+    const float inv = sum[n] > 0.f ? 1.f / sum[n] : (sum[n] == 0.f ? 0.f : sum[n]);
+    f16x4 o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = (_Float16)(acc[n][e] * inv);
+    *reinterpret_cast<f16x4*>(a.out + (int64_t)(sq.start + y / a.Hq) * a.ldo +
+                              (int64_t)(y % a.Hq) * D + 4 * lane) = o;
+  }
+}
+
+template <int D, int U>
+void launch_join(const AttnArgs& a, const AttnPlan& p, const float* partials, hipStream_t stream) {
+  const int rows = 4 * (8 / U);            // of a block
+  hipLaunchKernelGGL((attn_join_kernel<D, U>), dim3((a.max_q * a.Hq + rows - 1) / rows, a.B), dim3(256),
+                     0, stream, a, p.splits, p.row_tiles, p.rows, partials);
 }
 
 template <int D, int RT>
@@ -886,9 +918,16 @@ void launch_d(const AttnArgs& a, const AttnPlan& p, void* ws, hipStream_t stream
   else if (p.rows == 64) launch_tile<D, D == 256 ? 2 : 4, D == 256 ? 1 : 2>(a, p, partials, stream);
   else if (p.rows == 128) launch_tile<D, 4, 1>(a, p, partials, stream);
   else if constexpr (D != 256) launch_tile<D, 8, 1>(a, p, partials, stream);
-  if (p.splits > 1 && !p.last_joins)
-    hipLaunchKernelGGL(attn_join_kernel<D>, dim3((a.max_q * a.Hq + 3) / 4, a.B), dim3(256), 0,
-                       stream, a, p.splits, p.row_tiles, p.rows, partials);
+  if (p.splits > 1 && !p.last_joins) {
+    // Eight rows a wave where one load holds all splits (never at D = 256) and the rows still fill the
+    // CUs: 32,000 rows in two, D = 128, over 4,000 tokens 89 -> 87 us; 8,000 in two, D = 64, over 1,400
+    // 20 -> 22.
+    constexpr int U = D == 256 ? 8 : 1;
+    if (p.splits <= 256 / D && (int64_t)a.B * a.max_q * a.Hq >= 16384)
+      launch_join<D, U>(a, p, partials, stream);
+    else
+      launch_join<D, 8>(a, p, partials, stream);
+  }
 }
 
 }  // namespace
