@@ -477,6 +477,14 @@ __global__ __launch_bounds__(kThreads, 1) void attn_stream_kernel(AttnArgs a, in
   }
 }
 
+// Few splits of many rows: tens of megabytes of partial results, which pass the L2s by (2 x 500 tokens
+// x 32 heads of 64 in four splits over 32,500 278 -> 268 us; fewer rows lose, 250 tokens in eight 24 ->
+// 30), and eight rows a wave to join, one load for all splits of a row (32,000 rows in two, D = 128,
+// over 4,000 tokens 89 -> 87 us; 8,000 in two, D = 64, over 1,400 20 -> 22).
+__host__ __device__ __forceinline__ bool many_rows(const AttnArgs& a, int splits, int D) {
+  return splits <= 256 / D && (int64_t)a.B * a.max_q * a.Hq >= 16384;
+}
+
 // ------------------------------------------------------------------ many rows
 // NW waves, in KS groups: the waves of a group take 32 packed rows each, the groups every KS-th 32 keys
 // of a tile; keys per tile and tiles in the ring.  A wave copies KT / NW keys of a tile, at most 16,
@@ -790,12 +798,16 @@ __global__ __launch_bounds__(64 * NW, (TileRing<D, NW, KS>::kPerSimd)) void attn
     const int64_t item = (((int64_t)b * a.Hkv + h) * gridDim.y + tile) * splits + split;
     float* po = part + item * kTileRows * (D + 2);
     const int r = 32 * row_wave + col;
+    const bool past = many_rows(a, splits, D);
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<f32x4*>(po + (int64_t)r * D + 32 * d + 8 * g + 4 * half) =
-            f32x4{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 y{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
+        f32x4* to = reinterpret_cast<f32x4*>(po + (int64_t)r * D + 32 * d + 8 * g + 4 * half);
+        if (NW == 8 && past) __builtin_nontemporal_store(y, to);
+        else *to = y;
+      }
     if (half == 0) {
       po[(int64_t)kTileRows * D + 2 * r] = m;
       po[(int64_t)kTileRows * D + 2 * r + 1] = l;
@@ -845,9 +857,11 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int splits, 
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int k = 0; k < U; ++k)
-        v[n][k] = *reinterpret_cast<const f32x4*>(
+      for (int k = 0; k < U; ++k) {
+        const f32x4* x = reinterpret_cast<const f32x4*>(
             p[n] + min(s0 + k * SP + lane / LR, splits - 1) * step);
+        v[n][k] = U == 1 ? __builtin_nontemporal_load(x) : *x;
+      }
     if (s0 == 0) {
       // lanes behind the splits hold none: the sums of the first lanes are whole
 #pragma unroll
@@ -919,14 +933,9 @@ void launch_d(const AttnArgs& a, const AttnPlan& p, void* ws, hipStream_t stream
   else if (p.rows == 128) launch_tile<D, 4, 1>(a, p, partials, stream);
   else if constexpr (D != 256) launch_tile<D, 8, 1>(a, p, partials, stream);
   if (p.splits > 1 && !p.last_joins) {
-    // Eight rows a wave where one load holds all splits (never at D = 256) and the rows still fill the
-    // CUs: 32,000 rows in two, D = 128, over 4,000 tokens 89 -> 87 us; 8,000 in two, D = 64, over 1,400
-    // 20 -> 22.
-    constexpr int U = D == 256 ? 8 : 1;
-    if (p.splits <= 256 / D && (int64_t)a.B * a.max_q * a.Hq >= 16384)
-      launch_join<D, U>(a, p, partials, stream);
-    else
-      launch_join<D, 8>(a, p, partials, stream);
+    constexpr int U = D == 256 ? 8 : 1;    // (at D = 256 a load holds one split)
+    if (many_rows(a, p.splits, D)) launch_join<D, U>(a, p, partials, stream);
+    else launch_join<D, 8>(a, p, partials, stream);
   }
 }
 
